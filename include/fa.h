@@ -1,7 +1,7 @@
 /*
- * fa.h -- C ABI of the GB300 (sm_103a) exact-attention forward library.
+ * fa.h -- C ABI of the GB300 (sm_103a) exact-attention library.
  *
- * What is computed (all entry points): for every query row i and query head h,
+ * What is computed (all attention entry points): for every query row i and query head h,
  *     O[i,h,:] = softmax_j( scale * q_i . k_j  over the keys j that row i may attend to ) . V
  *     LSE[i,h] = ln sum_j exp(scale * q_i . k_j)      (same key set)
  * This is the naive pipeline of "I/O-Aware Kernels" (datasystem.school, Module 5), section
@@ -70,6 +70,39 @@ const char* fa_status_string(fa_status s);
  */
 fa_status fa_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq,
                  int Hkv, int S, int d, int causal, float scale, fa_stream_t stream);
+
+/*
+ * Dense attention backward: the gradients of fa_fwd's result, with the probabilities recomputed tile
+ * by tile from the log-sum-exps (the S x S matrices never reach device memory). The pages describe
+ * the forward pass only; a model that is trained with it needs this pass too.
+ *   q, o, dout, dq: [B, S, Hq, d] bf16;  k, v, dk, dv: [B, S, Hkv, d] bf16;
+ *   lse, dlse: [B, S, Hq] fp32. o and lse are what fa_fwd returned for q, k, v with the same causal
+ *   and scale; dout is the gradient with respect to o, and dlse (may be NULL: zero) the gradient
+ *   with respect to lse, for losses that use it.
+ * With P_ij = exp(scale * q_i . k_j - lse_i) (0 where masked) and delta_i = dout_i . o_i - dlse_i:
+ *     dv_j = sum_i P_ij dout_i              dS_ij = P_ij (dout_i . v_j - delta_i)
+ *     dq_i = scale * sum_j dS_ij k_j        dk_j = scale * sum_i dS_ij q_i
+ * where the sums over i run over every query head of the key/value head's group. A row whose lse is
+ * -inf gives no gradient. P and dS are rounded to bf16 before their matrix products; everything
+ * else is fp32. Every gradient is summed in a fixed order: the same inputs give the same bits.
+ * A non-finite value of q, k, v, o or dout can reach any gradient of its batch entry and kv head.
+ *   dq, dk, dv are written whole. They and the workspace share no memory with each other or with
+ *   any input (FA_ERR_INVALID_ARG).
+ *   workspace: device scratch of at least fa_bwd_workspace_bytes(...) bytes, 256-byte aligned. Its
+ *   contents need no initialisation; calls that share one must be ordered on one stream.
+ * Errors: FA_ERR_INVALID_ARG (null pointer, non-positive size, Hq % Hkv != 0, scale not finite and
+ * positive, overlapping memory), FA_ERR_UNSUPPORTED (d not 64 or 128, or too large),
+ * FA_ERR_ALIGNMENT, FA_ERR_WORKSPACE, FA_ERR_CUDA. Asynchronous on `stream` (two kernels; can be
+ * captured in a CUDA graph).
+ */
+fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                 const void* dout, const float* dlse, void* dq, void* dk, void* dv, int B, int Hq,
+                 int Hkv, int S, int d, int causal, float scale, void* workspace,
+                 size_t workspace_bytes, fa_stream_t stream);
+
+/* Workspace bytes fa_bwd needs for these sizes (0 for sizes it refuses): the row statistics of every
+ * query. */
+size_t fa_bwd_workspace_bytes(int B, int Hq, int Hkv, int S, int d, int causal);
 
 /*
  * Paged, ragged attention forward ("FlashInfer: I/O-aware attention for serving").

@@ -7,6 +7,8 @@ package is its thin binding plus the seeded workload generator used by tests and
 from .binding import (  # noqa: F401
     EXPORTED,
     FaError,
+    fa_bwd,
+    fa_bwd_workspace_bytes,
     fa_cascade_fwd,
     fa_cascade_workspace_bytes,
     fa_decode_num_splits,

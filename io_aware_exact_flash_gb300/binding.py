@@ -28,7 +28,7 @@ _STATUS_NAMES = {
 EXPORTED = ("fa_status_string", "fa_fwd", "fa_paged_fwd", "fa_paged_workspace_bytes",
             "fa_decode_num_splits", "fa_merge_states", "fa_get_device_status", "fa_paged_decode_noalloc",
             "fa_selftest_wait_timeout", "fa_paged_append", "fa_cascade_fwd", "fa_cascade_workspace_bytes",
-            "fa_paged_num_splits")
+            "fa_paged_num_splits", "fa_bwd", "fa_bwd_workspace_bytes")
 
 
 class FaError(RuntimeError):
@@ -81,6 +81,10 @@ def load_library(path: str = None) -> ctypes.CDLL:
     lib.fa_cascade_fwd.restype = i
     lib.fa_paged_append.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, i, vp, vp, vp]
     lib.fa_paged_append.restype = i
+    lib.fa_bwd_workspace_bytes.argtypes = [i] * 6
+    lib.fa_bwd_workspace_bytes.restype = sz
+    lib.fa_bwd.argtypes = [vp] * 10 + [i] * 6 + [f, vp, sz, vp]
+    lib.fa_bwd.restype = i
     lib.fa_get_device_status.argtypes = [vp, ctypes.POINTER(i), ctypes.POINTER(i)]
     lib.fa_get_device_status.restype = i
     _lib = lib
@@ -157,6 +161,82 @@ def fa_fwd(q, k, v, causal=False, scale=None, out=None, lse=None, return_lse=Tru
                       _stream(stream))
     _check("fa_fwd", code)
     return out, lse
+
+
+def _one_device(like, tensors):
+    """Every tensor of a call lives on one device (None entries are absent arguments)."""
+    for name, t in tensors:
+        if t is not None and t.device != like.device:
+            raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+
+
+@contextlib.contextmanager
+def _on_device(device, stream):
+    """Make `device` current, and `stream` (default: that device's current stream) the stream that
+    allocations of the call belong to; yields the stream's handle."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.device(device), _on(stream):
+        yield _stream(stream)
+
+
+def _result(name, t, shape, dtype, device):
+    """A caller-given output after its checks, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape)
+            or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t
+
+
+def _scratch(workspace, need, device):
+    """A caller-given workspace (any contiguous CUDA tensor), or a new one; with its size in bytes."""
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def fa_bwd_workspace_bytes(B, Hq, Hkv, S, d, causal=False):
+    return int(load_library().fa_bwd_workspace_bytes(B, Hq, Hkv, S, d, int(bool(causal))))
+
+
+def fa_bwd(q, k, v, out, lse, dout, causal=False, scale=None, dlse=None, dq=None, dk=None, dv=None, workspace=None,
+           stream=None):
+    """Dense attention backward: the gradients of fa_fwd.
+
+    q, out, dout: [B, S, Hq, d]; k, v: [B, S, Hkv, d] (bf16, CUDA); lse: [B, S, Hq] fp32. out and
+    lse are fa_fwd's results for q, k, v with the same causal and scale. dlse ([B, S, Hq] fp32) is the
+    gradient with respect to lse, if a loss uses it. Returns (dq, dk, dv) in the layouts of q, k, v.
+    Nothing is summed by atomics: the same inputs give the same bits."""
+    for name, t in (("q", q), ("k", k), ("v", v), ("out", out), ("dout", dout)):
+        _bf16_cuda(name, t, 4)
+    B, S, Hq, d = q.shape
+    Hkv = k.shape[2]
+    if k.shape != (B, S, Hkv, d) or v.shape != k.shape:
+        raise ValueError("k and v must be [B, S, Hkv, d] matching q")
+    if out.shape != q.shape or dout.shape != q.shape:
+        raise ValueError("out and dout must have q's shape")
+    for name, t in (("lse", lse), ("dlse", dlse)):
+        if t is None and name == "dlse":
+            continue
+        if (not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_cuda or t.shape != (B, S, Hq)
+                or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of shape {(B, S, Hq)}")
+    _one_device(q, (("k", k), ("v", v), ("out", out), ("lse", lse), ("dout", dout), ("dlse", dlse)))
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    lib = load_library()
+    with _on_device(q.device, stream) as handle:
+        dq = _result("dq", dq, q.shape, q.dtype, q.device)
+        dk = _result("dk", dk, k.shape, k.dtype, q.device)
+        dv = _result("dv", dv, v.shape, v.dtype, q.device)
+        workspace, ws_bytes = _scratch(workspace, fa_bwd_workspace_bytes(B, Hq, Hkv, S, d, causal), q.device)
+        code = lib.fa_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dlse), _ptr(dq), _ptr(dk),
+                          _ptr(dv), B, Hq, Hkv, S, d, int(bool(causal)), scale, _ptr(workspace), ws_bytes, handle)
+    _check("fa_bwd", code)
+    return dq, dk, dv
 
 
 def fa_paged_workspace_bytes(num_seqs, total_q, max_q_len, page_size, max_pages_per_seq, num_pages, Hq, Hkv, d,

@@ -9,6 +9,7 @@
 #include <atomic>
 #include <mutex>
 #include "../../include/fa.h"
+#include "host.cuh"
 #include "kernels.cuh"
 
 // The one piece of global device state: a status word per GPU that kernels set instead of
@@ -188,6 +189,11 @@ int fa::current_device_info(DeviceStatus** status, int* sm_count) {
   *status = dev->status;
   *sm_count = dev->sm_count;
   return FA_OK;
+}
+
+bool fa::make_bf16_map(CUtensorMap* m, const void* base, const uint64_t dims[4], const uint64_t strides[3],
+                       const uint32_t box[4]) {
+  return make_map(m, base, dims, strides, box);
 }
 
 namespace {

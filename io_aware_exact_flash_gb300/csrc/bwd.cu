@@ -1,0 +1,692 @@
+// Attention backward for sm_103a: the gradients of O = softmax(scale Q K^T [+ causal mask]) V, with
+// the probabilities recomputed tile by tile from the forward pass's log-sum-exps.
+//
+// With P_ij = exp(scale q_i . k_j - LSE_i) (0 where masked) and delta_i = dO_i . O_i - dLSE_i:
+//     dV_j = sum_i P_ij dO_i
+//     dS_ij = P_ij (dO_i . v_j - delta_i)
+//     dQ_i = scale sum_j dS_ij k_j          dK_j = scale sum_i dS_ij q_i
+// (sums over i run over every query head that shares the key/value head).
+//
+// Two kinds of work unit share one launch. A key unit owns 128 keys of one key/value head, keeps
+// their K and V tiles in shared memory and dK, dV in tensor memory (TMEM), and streams the query
+// tiles (Q, dO and the row statistics) that see those keys: S^T = K Q^T, dP^T = V dO^T,
+// dV += P^T dO, dK += dS^T Q. A query unit owns 128 queries of one query head and streams key
+// tiles: S = Q K^T, dP = dO V^T, dQ += dS K. That is seven matrix products per pair of tiles where
+// five would do, but every gradient is summed inside one CTA in a fixed order: no atomics, the
+// same bits every run, and no fp32 dQ traffic (a 64 KB read-modify-write per tile pair).
+//
+// CTA organisation (384 threads, one CTA per SM):
+//   warp 0      TMA producer: the two resident tiles, then the streamed tiles into a ring of slots
+//   warp 1      TMEM owner; one lane issues every tcgen05.mma
+//   warps 4-11  two warpgroups; thread t of a warpgroup owns row t of the 128 x 128 score tile
+//               (a TMEM lane), warpgroup g its columns [64 g, 64 g + 64)
+// P and dS are rounded to bf16 (the input type, as in the forward pass's P V) for their matrix
+// products, and written back to TMEM as the A operands; sums and statistics stay in fp32.
+#include <cuda_bf16.h>
+#include <atomic>
+#include <cmath>
+#include <cstring>
+#include "../../include/fa.h"
+#include "host.cuh"
+#include "kernels.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kTile = 128;        // queries and keys per tile
+constexpr int kBwdThreads = 384;
+constexpr int kStatBytes = 1024;  // -LSE (base 2) and -delta of one query tile
+constexpr int kRegsBwdControl = 64;
+constexpr int kRegsBwdMath = 216;
+static_assert(128 * kRegsBwdControl + 256 * kRegsBwdMath <= kBwdThreads * 168, "register split too large");
+
+enum : uint32_t {
+  kSiteBwdEmpty = 30,
+  kSiteBwdResident = 31,
+  kSiteBwdFull = 32,
+  kSiteBwdP = 33,
+  kSiteBwdDs = 34,
+  kSiteBwdS = 35,
+  kSiteBwdDp = 36,
+  kSiteBwdStat = 37,
+  kSiteBwdAcc = 38,
+  kSiteBwdDrain = 39,
+  kSiteBwdSmem = 40,
+};
+
+struct alignas(64) BwdParams {
+  CUtensorMap tm_q, tm_k, tm_v, tm_do;  // (d, heads, S, B), boxes of 64 x 1 x 128 x 1
+  const float* stat;                    // [B, Hq, T, 2, 128]: -LSE log2(e), then -delta
+  __nv_bfloat16 *dq, *dk, *dv;
+  int B, S, T, Hq, Hkv, group, causal;
+  int kv_units;                         // key units come first in the grid
+  int kv_chunk, q_chunk;                // heads whose units are scheduled together
+  float scale, scale_log2;
+  DeviceStatus* status;
+};
+
+struct StatParams {
+  const __nv_bfloat16 *o, *dout;  // [B, S, Hq, d]
+  const float *lse, *dlse;        // [B, S, Hq] (dlse may be null)
+  float* stat;
+  int B, S, T, Hq;
+};
+
+template <int D>
+struct BwdCfg {
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int kSub = D / 64;          // 128-byte-wide column blocks per tile
+  static constexpr int kSubBytes = kTile * 128;
+  static constexpr int kSlots = D == 128 ? 5 : 10;
+  // score buffers of a key unit: TMEM holds dK, dV (2 D columns) and three 128-column tiles at
+  // d = 64, two at d = 128. A query unit (dQ alone) always has room for three.
+  static constexpr int kKeyScoreBufs = D == 128 ? 1 : 2;
+  static constexpr int kOffStat = (2 + kSlots) * kTileBytes;
+  static constexpr int kOffCtl = kOffStat + 2 * kStatBytes;
+  static constexpr int kSmemBytes = kOffCtl + 512;
+};
+
+// Barriers and flags at the end of the CTA's shared memory (no static shared memory: the tiles at
+// its start must be 1024-byte aligned and leave no room for padding at d = 128).
+template <int D>
+struct Ctl {
+  uint64_t full[BwdCfg<D>::kSlots], empty[BwdCfg<D>::kSlots];
+  uint64_t resident, s[2], dp, p[2], ds, acc, stat_full[2], stat_empty[2];
+  uint32_t tmem;
+  int abort;
+};
+
+// Which tiles a CTA owns and streams.
+struct BwdUnit {
+  bool key;        // key unit (dK, dV) or query unit (dQ)
+  int b, h, tile;  // h: key/value head of a key unit, query head of a query unit
+  int first, per;  // streamed tiles per head: [first, first + per)
+  int steps;
+};
+
+// Units are ordered by chunks of heads, about one wave of CTAs per chunk, so that CTAs running
+// together stream the same few heads' tiles from L2; inside a chunk the units with the most steps
+// come first. Key units precede query units: they are the long ones when heads share keys.
+__device__ __forceinline__ BwdUnit bwd_unit(const BwdParams& p) {
+  BwdUnit u;
+  int r = blockIdx.x;
+  u.key = r < p.kv_units;
+  if (!u.key) r -= p.kv_units;
+  const int heads = u.key ? p.Hkv : p.Hq;
+  const int chunk_heads = u.key ? p.kv_chunk : p.q_chunk;
+  const int chunk = r / (chunk_heads * p.T);
+  const int head0 = chunk * chunk_heads;
+  const int width = min(chunk_heads, p.B * heads - head0);
+  const int rc = r - chunk * chunk_heads * p.T;
+  const int rank = rc / width;
+  const int head = head0 + rc % width;
+  u.b = head / heads;
+  u.h = head % heads;
+  u.tile = (u.key || !p.causal) ? rank : p.T - 1 - rank;
+  u.first = (u.key && p.causal) ? u.tile : 0;
+  u.per = !p.causal ? p.T : (u.key ? p.T - u.tile : u.tile + 1);
+  u.steps = u.key ? u.per * p.group : u.per;
+  return u;
+}
+
+// X[128 x 128] = A B^T over d: both tiles K-major in shared memory (the address arithmetic of the
+// descriptors is that of the forward kernel: 32 bytes per K step inside a 128-byte swizzled row,
+// 16 KB per 64-column block).
+template <int D>
+__device__ __forceinline__ void mma_scores(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc) {
+  constexpr uint32_t idesc = make_idesc_bf16(kTile, kTile, false);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint64_t off = (uint64_t)((kk >> 2) * (BwdCfg<D>::kSubBytes >> 4) + (kk & 3) * 2);
+    mma_ss(d_tmem, a_desc + off, b_desc + off, idesc, kk > 0 ? 1u : 0u);
+  }
+}
+
+// acc[128 x d] += A B: A (bf16 pairs) in TMEM, 16 columns of the score tile per step. Each
+// warpgroup writes its 64 columns' pairs over the first half of its own 64 TMEM columns, so the
+// second half of A starts 64 columns in. B is the streamed tile as the MN-major operand.
+template <int D>
+__device__ __forceinline__ void mma_accumulate(uint32_t acc, uint32_t a_tmem, uint64_t b_desc, bool accumulate) {
+  constexpr uint32_t idesc = make_idesc_bf16(kTile, D, true);
+#pragma unroll
+  for (int kk = 0; kk < kTile / 16; ++kk)
+    mma_ts(acc, a_tmem + kk * 8 + (kk >> 2) * 32, b_desc + (uint64_t)kk * (2048 >> 4), idesc,
+           (kk > 0 || accumulate) ? 1u : 0u);
+}
+
+template <int D>
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int h, int row, int b,
+                                          uint64_t policy) {
+#pragma unroll
+  for (int sub = 0; sub < BwdCfg<D>::kSub; ++sub)
+    tma_load_4d_hint(dst + sub * BwdCfg<D>::kSubBytes, map, bar, sub * 64, h, row, b, policy);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kBwdThreads, 1) bwd_kernel(const __grid_constant__ BwdParams p) {
+  using C = BwdCfg<D>;
+  constexpr int NS = C::kSlots;
+  constexpr int TB = C::kTileBytes;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Ctl<D>& ctl = *reinterpret_cast<Ctl<D>*>(smem + C::kOffCtl);
+  static_assert(sizeof(Ctl<D>) <= 512, "control block too large");
+  uint8_t* slots = smem + 2 * TB;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (smem_u32(smem) & 1023u) {  // the swizzled tiles need 1024-byte alignment
+    if (threadIdx.x == 0 && atomicCAS(&p.status->code, 0u, 7u) == 0u) p.status->where = kSiteBwdSmem;
+    return;
+  }
+  if (threadIdx.x == 0) {
+    ctl.abort = 0;
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&ctl.full[s], 1);
+      mbar_init(&ctl.empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctl.s[s], 1);
+      mbar_init(&ctl.p[s], 8);  // two: a warp may reach step i + 1 before another has finished step i
+      mbar_init(&ctl.stat_full[s], 1);
+      mbar_init(&ctl.stat_empty[s], 8);  // one arrival per math warp
+    }
+    mbar_init(&ctl.resident, 1);
+    mbar_init(&ctl.dp, 1);
+    mbar_init(&ctl.ds, 8);
+    mbar_init(&ctl.acc, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctl.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem;
+  volatile int* abort = &ctl.abort;
+  const BwdUnit u = bwd_unit(p);
+  // TMEM columns: key unit: dV [0, D), dK [D, 2D), then score buffer 0, dP, score buffer 1;
+  // query unit: dQ [0, D), then the same three tiles.
+  const uint32_t t_s0 = tmem + (u.key ? 2 * D : D);
+  const uint32_t t_dp = t_s0 + 128;
+  const int bufs = u.key ? C::kKeyScoreBufs : 2;
+  auto t_s = [&](int i) { return t_s0 + ((bufs == 2 && (i & 1)) ? 256u : 0u); };
+  auto s_bar = [&](int i) { return &ctl.s[bufs == 2 ? (i & 1) : 0]; };
+  auto s_par = [&](int i) { return (uint32_t)((bufs == 2 ? (i >> 1) : i) & 1); };
+
+  if (warp == 0) {
+    regs_dec<kRegsBwdControl>();
+    // ================================================================ TMA producer
+    if (lane == 0) {
+      const uint64_t policy = policy_evict_last();  // every tile is read by many units
+      mbar_arrive_expect_tx(&ctl.resident, 2 * TB);
+      load_tile<D>(smem, u.key ? &p.tm_k : &p.tm_q, &ctl.resident, u.h, u.tile * kTile, u.b, policy);
+      load_tile<D>(smem + TB, u.key ? &p.tm_v : &p.tm_do, &ctl.resident, u.h, u.tile * kTile, u.b, policy);
+      // key unit: dO_i then Q_i (dO_i is released first); query unit: K_j then V_j
+      const CUtensorMap* map0 = u.key ? &p.tm_do : &p.tm_k;
+      const CUtensorMap* map1 = u.key ? &p.tm_q : &p.tm_v;
+      int it = 0, t = u.first, h = u.key ? u.h * p.group : u.h / p.group;
+      for (int i = 0; i < u.steps; ++i) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half, ++it) {
+          const int s = it % NS;
+          if (it >= NS) mbar_wait(&ctl.empty[s], (it / NS + 1) & 1, abort, p.status, kSiteBwdEmpty);
+          mbar_arrive_expect_tx(&ctl.full[s], TB);
+          load_tile<D>(slots + s * TB, half ? map1 : map0, &ctl.full[s], h, t * kTile, u.b, policy);
+        }
+        if (u.key) {
+          if (i == 0) {  // the statistics come from the kernel before this one
+            griddep_wait();
+            asm volatile("fence.proxy.async.global;" ::: "memory");
+          }
+          const int s = i & 1;
+          if (i >= 2) mbar_wait(&ctl.stat_empty[s], (i / 2 + 1) & 1, abort, p.status, kSiteBwdStat);
+          mbar_arrive_expect_tx(&ctl.stat_full[s], kStatBytes);
+          bulk_load(smem + C::kOffStat + s * kStatBytes, p.stat + (((int64_t)u.b * p.Hq + h) * p.T + t) * 256,
+                    kStatBytes, &ctl.stat_full[s]);
+        }
+        if (++t == u.first + u.per) {
+          t = u.first;
+          ++h;
+        }
+      }
+      if (*abort) {  // after an abort nothing has waited for the copies in flight: do it here (bounded)
+        int no_abort = 0;
+        mbar_wait(&ctl.resident, 0, &no_abort, p.status, kSiteBwdDrain);
+        for (int k = it > NS ? it - NS : 0; k < it; ++k)
+          mbar_wait(&ctl.full[k % NS], (k / NS) & 1, &no_abort, p.status, kSiteBwdDrain);
+        if (u.key)
+          for (int k = u.steps > 2 ? u.steps - 2 : 0; k < u.steps; ++k)
+            mbar_wait(&ctl.stat_full[k & 1], (k / 2) & 1, &no_abort, p.status, kSiteBwdDrain);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    regs_dec<kRegsBwdControl>();
+    // ================================================================ MMA issuer
+    if (lane == 0) {
+      const uint64_t a0 = make_sdesc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t a1 = a0 + (TB >> 4);
+      const uint64_t bk = make_sdesc_sw128(smem_u32(slots), 16, 1024);              // K-major view of slot 0
+      const uint64_t bm = make_sdesc_sw128(smem_u32(slots), C::kSubBytes, 1024);    // MN-major view of slot 0
+      const int n = u.steps;
+      auto wait_full = [&](int it) {
+        mbar_wait(&ctl.full[it % NS], (it / NS) & 1, abort, p.status, kSiteBwdFull);
+        tc_fence_after();
+      };
+      auto slot = [&](int it) { return (uint64_t)((it % NS) * (TB >> 4)); };
+      mbar_wait(&ctl.resident, 0, abort, p.status, kSiteBwdResident);
+      if (u.key) {
+        auto scores = [&](int i) {  // S^T = K Q_i^T
+          wait_full(2 * i + 1);
+          mma_scores<D>(t_s(i), a0, bk + slot(2 * i + 1));
+          mma_commit(s_bar(i));
+        };
+        auto dprob = [&](int i) {  // dP^T = V dO_i^T
+          wait_full(2 * i);
+          mma_scores<D>(t_dp, a1, bk + slot(2 * i));
+          mma_commit(&ctl.dp);
+        };
+        scores(0);
+        dprob(0);
+        if (bufs == 2 && n > 1) scores(1);
+        for (int i = 0; i < n; ++i) {
+          mbar_wait(&ctl.p[i & 1], (i >> 1) & 1, abort, p.status, kSiteBwdP);
+          tc_fence_after();
+          mma_accumulate<D>(tmem, t_s(i), bm + slot(2 * i), i > 0);  // dV += P^T dO_i
+          mma_commit(&ctl.empty[(2 * i) % NS]);
+          if (i + bufs < n) scores(i + bufs);  // into the buffer P_i leaves
+          mbar_wait(&ctl.ds, i & 1, abort, p.status, kSiteBwdDs);
+          tc_fence_after();
+          mma_accumulate<D>(tmem + D, t_dp, bm + slot(2 * i + 1), i > 0);  // dK += dS^T Q_i
+          mma_commit(&ctl.empty[(2 * i + 1) % NS]);
+          if (i + 1 < n) dprob(i + 1);
+        }
+      } else {
+        auto scores = [&](int j) {  // S = Q K_j^T
+          wait_full(2 * j);
+          mma_scores<D>(t_s(j), a0, bk + slot(2 * j));
+          mma_commit(s_bar(j));
+        };
+        auto dprob = [&](int j) {  // dP = dO V_j^T, after which V_j is done with
+          wait_full(2 * j + 1);
+          mma_scores<D>(t_dp, a1, bk + slot(2 * j + 1));
+          mma_commit(&ctl.dp);
+          mma_commit(&ctl.empty[(2 * j + 1) % NS]);
+        };
+        scores(0);
+        dprob(0);
+        if (n > 1) scores(1);
+        for (int j = 0; j < n; ++j) {
+          // dS_j is written (over S_j), and dP_j has been read: dP_{j+1} goes first, because the
+          // math warps need it next
+          mbar_wait(&ctl.ds, j & 1, abort, p.status, kSiteBwdDs);
+          tc_fence_after();
+          if (j + 1 < n) dprob(j + 1);
+          mma_accumulate<D>(tmem, t_s(j), bm + slot(2 * j), j > 0);  // dQ += dS K_j
+          mma_commit(&ctl.empty[(2 * j) % NS]);
+          if (j + 2 < n) scores(j + 2);
+        }
+      }
+      // every MMA has completed before TMEM is released
+      mma_commit(&ctl.acc);
+      int no_abort = 0;
+      mbar_wait(&ctl.acc, 0, &no_abort, p.status, kSiteBwdDrain);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    regs_inc<kRegsBwdMath>();
+    // ================================================================ P, dS and the epilogue
+    const int g = (warp - 4) >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t half_off = lane_off + 64 * g;
+    const uint64_t c2 = f32x2(p.scale_log2, p.scale_log2);
+    // query unit: this row's statistics
+    float nlse = 0.f, ndelta = 0.f;
+    if (!u.key) {
+      griddep_wait();
+      const float* st = p.stat + (((int64_t)u.b * p.Hq + u.h) * p.T + u.tile) * 256;
+      nlse = st[row];
+      ndelta = st[128 + row];
+    }
+    int t = u.first;
+    for (int i = 0; i < u.steps; ++i) {
+      // columns [lo, hi) of this row's 64 are not masked
+      int lo = 0, hi = 64;
+      if (p.causal && t == u.tile) {
+        if (u.key) lo = row - 64 * g;
+        else hi = row + 1 - 64 * g;
+      }
+      if (!u.key && (t + 1) * kTile > p.S) hi = min(hi, p.S - t * kTile - 64 * g);
+      const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < 64);
+      const float* st = reinterpret_cast<const float*>(smem + C::kOffStat + (i & 1) * kStatBytes) + 64 * g;
+      if (u.key) mbar_wait(&ctl.stat_full[i & 1], (i >> 1) & 1, abort, p.status, kSiteBwdStat);
+      mbar_wait(s_bar(i), s_par(i), abort, p.status, kSiteBwdS);
+      __syncwarp();
+      tc_fence_after();
+      uint64_t pr[32];  // P of this row's 64 columns, in pairs
+      const uint32_t ts = t_s(i) + half_off;
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        uint32_t sr[32];
+        tmem_ld32(ts + 32 * cc, sr);
+        tmem_ld_wait(sr);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          uint64_t nl;
+          if (u.key) nl = *reinterpret_cast<const uint64_t*>(st + 32 * cc + 2 * k);
+          else nl = f32x2(nlse, nlse);
+          float x0, x1;
+          split_f32x2(fma_f32x2(f32x2(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1])), c2, nl), x0, x1);
+          pr[16 * cc + k] = f32x2(ex2(x0), ex2(x1));
+        }
+      }
+      if (masked) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          float a, b;
+          split_f32x2(pr[k], a, b);
+          if (2 * k < lo || 2 * k >= hi) a = 0.f;
+          if (2 * k + 1 < lo || 2 * k + 1 >= hi) b = 0.f;
+          pr[k] = f32x2(a, b);
+        }
+      }
+      if (u.key) {  // P^T is dV's A operand, written over this half's scores
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            float a, b;
+            split_f32x2(pr[16 * cc + k], a, b);
+            pk[k] = pack_bf16x2(a, b);
+          }
+          tmem_st16(ts + 16 * cc, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.p[i & 1]);
+      }
+      mbar_wait(&ctl.dp, i & 1, abort, p.status, kSiteBwdDp);
+      __syncwarp();
+      tc_fence_after();
+      const uint32_t td = t_dp + half_off;
+      const uint32_t t_out = u.key ? td : ts;  // dS goes over dP (key unit) or over the scores
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        uint32_t dr[32], pk[16];
+        tmem_ld32(td + 32 * cc, dr);
+        tmem_ld_wait(dr);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          uint64_t nd;
+          if (u.key) nd = *reinterpret_cast<const uint64_t*>(st + 128 + 32 * cc + 2 * k);
+          else nd = f32x2(ndelta, ndelta);
+          const uint64_t v = mul_f32x2(
+              pr[16 * cc + k], add_f32x2(f32x2(__uint_as_float(dr[2 * k]), __uint_as_float(dr[2 * k + 1])), nd));
+          float a, b;
+          split_f32x2(v, a, b);
+          pk[k] = pack_bf16x2(a, b);
+        }
+        if (masked) {  // not 0 times dP: dP may be infinite or NaN where masked
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int c = 32 * cc + 2 * k;
+            if (c < lo || c >= hi) pk[k] &= 0xffff0000u;
+            if (c + 1 < lo || c + 1 >= hi) pk[k] &= 0x0000ffffu;
+          }
+        }
+        tmem_st16(t_out + 16 * cc, pk);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&ctl.ds);
+        if (u.key) mbar_arrive(&ctl.stat_empty[i & 1]);
+      }
+      if (++t == u.first + u.per) t = u.first;
+    }
+    // ------------------------------------------------------------ epilogue
+    mbar_wait(&ctl.acc, 0, abort, p.status, kSiteBwdAcc);
+    __syncwarp();
+    tc_fence_after();
+    // key unit: warpgroup 0 stores dV, warpgroup 1 dK; query unit: half of dQ's columns each
+    const int cols = u.key ? D : D / 2;
+    const uint32_t tacc = tmem + lane_off + g * cols;
+    const int heads = u.key ? p.Hkv : p.Hq;
+    const int srow = u.tile * kTile + row;
+    __nv_bfloat16* base = u.key ? (g == 0 ? p.dv : p.dk) : p.dq + g * cols;
+    base += (((int64_t)u.b * p.S + srow) * heads + u.h) * D;
+    const float mul = (u.key && g == 0) ? 1.f : p.scale;
+    const bool store = srow < p.S;
+#pragma unroll 1
+    for (int cc = 0; cc < cols / 32; ++cc) {
+      uint32_t r[32];
+      tmem_ld32(tacc + 32 * cc, r);
+      tmem_ld_wait(r);
+      if (store) {
+        uint4* dst = reinterpret_cast<uint4*>(base + 32 * cc);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t w[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            w[x] = pack_bf16x2(__uint_as_float(r[8 * k + 2 * x]) * mul, __uint_as_float(r[8 * k + 2 * x + 1]) * mul);
+          dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+  } else {
+    regs_dec<kRegsBwdControl>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Row statistics: -LSE in base 2 and -delta, laid out by query tile so that a key unit fetches a
+// tile's 256 values with one bulk copy. Rows past S get -inf and 0: their P and dS are then 0. A
+// row whose LSE is -inf (no key) gets the same. One warp takes 32 consecutive rows of one head;
+// warps with consecutive numbers take consecutive heads, so the rows they read are adjacent.
+constexpr int kStatThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kStatThreads) bwd_stat_kernel(StatParams p) {
+  griddep_launch_dependents();
+  constexpr int kLanes = D / 8;         // lanes per row, 16 bytes each
+  constexpr int kRows = 32 / kLanes;    // rows per pass of the warp
+  const int lane = threadIdx.x & 31;
+  const int64_t item = (int64_t)blockIdx.x * (kStatThreads / 32) + (threadIdx.x >> 5);
+  const int h = (int)(item % p.Hq);
+  const int64_t rest = item / p.Hq;
+  const int blocks = p.T * (kTile / 32);
+  const int b = (int)(rest / blocks), s0 = (int)(rest % blocks) * 32;
+  if (b >= p.B) return;
+  const int sub = lane / kLanes, part = lane % kLanes;
+  float mine = 0.f;  // delta of row s0 + lane
+  constexpr int kUnroll = 4;
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32; r0 += kRows * kUnroll) {
+    uint4 a[kUnroll], c[kUnroll];
+#pragma unroll
+    for (int x = 0; x < kUnroll; ++x) {
+      const int s = s0 + r0 + x * kRows + sub;
+      a[x] = c[x] = make_uint4(0, 0, 0, 0);
+      if (s < p.S) {
+        const int64_t off = (((int64_t)b * p.S + s) * p.Hq + h) * D + part * 8;
+        a[x] = __ldg(reinterpret_cast<const uint4*>(p.o + off));
+        c[x] = __ldg(reinterpret_cast<const uint4*>(p.dout + off));
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < kUnroll; ++x) {
+      const uint32_t av[4] = {a[x].x, a[x].y, a[x].z, a[x].w}, cv[4] = {c[x].x, c[x].y, c[x].z, c[x].w};
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        sum = fmaf(__uint_as_float(av[k] << 16), __uint_as_float(cv[k] << 16), sum);
+        sum = fmaf(__uint_as_float(av[k] & 0xffff0000u), __uint_as_float(cv[k] & 0xffff0000u), sum);
+      }
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      // row r0 + x * kRows + k of the block sits in lanes [k * kLanes, (k + 1) * kLanes)
+      const float got = __shfl_sync(0xffffffffu, sum, (lane % kRows) * kLanes);
+      if (lane / kRows == r0 / kRows + x) mine = got;
+    }
+  }
+  const int s = s0 + lane;
+  float nlse = -INFINITY, ndelta = 0.f;
+  if (s < p.S) {
+    const int64_t off = ((int64_t)b * p.S + s) * p.Hq + h;
+    const float l = p.lse[off];
+    if (l != -INFINITY) {
+      nlse = -l * 1.4426950408889634f;
+      ndelta = (p.dlse ? p.dlse[off] : 0.f) - mine;
+    }
+  }
+  float* dst = p.stat + (((int64_t)b * p.Hq + h) * p.T + s0 / kTile) * 256 + s0 % kTile + lane;
+  dst[0] = nlse;
+  dst[128] = ndelta;
+}
+
+template <int D>
+cudaError_t launch_bwd(const StatParams& sp, const BwdParams& p, int64_t units, cudaStream_t stream) {
+  static std::atomic<int> pool_ok{-1};
+  if (pool_ok.load(std::memory_order_relaxed) < 0) {
+    // the register split draws on the registers the CTA launches with
+    cudaFuncAttributes attr;
+    cudaError_t e = cudaFuncGetAttributes(&attr, bwd_kernel<D>);
+    if (e != cudaSuccess) return e;
+    pool_ok.store(attr.numRegs * kBwdThreads >= 128 * kRegsBwdControl + 256 * kRegsBwdMath ? 1 : 0,
+                  std::memory_order_relaxed);
+  }
+  if (pool_ok.load(std::memory_order_relaxed) != 1) return cudaErrorInvalidConfiguration;
+  static std::atomic<unsigned> configured_mask{0u};  // one bit per device ordinal below 32
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 32 || !(configured_mask.load(std::memory_order_acquire) & (1u << dev))) {
+    cudaError_t e =
+        cudaFuncSetAttribute(bwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdCfg<D>::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 32) configured_mask.fetch_or(1u << dev, std::memory_order_release);
+  }
+  const int64_t items = (int64_t)p.B * p.Hq * p.T * (kTile / 32);
+  const int64_t blocks = (items + kStatThreads / 32 - 1) / (kStatThreads / 32);
+  bwd_stat_kernel<D><<<(unsigned)blocks, kStatThreads, 0, stream>>>(sp);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // a programmatic dependent of the statistics kernel: set-up and the first tile loads overlap it
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)units);
+  cfg.blockDim = dim3(kBwdThreads);
+  cfg.dynamicSmemBytes = BwdCfg<D>::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, bwd_kernel<D>, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+int64_t bwd_tiles(int S) { return ((int64_t)S + kTile - 1) / kTile; }
+
+bool bwd_sizes_ok(int B, int Hq, int Hkv, int S) { return B > 0 && Hq > 0 && Hkv > 0 && S > 0 && Hq % Hkv == 0; }
+
+bool bwd_too_large(int B, int Hq, int Hkv, int S, int d) {
+  return (long long)B * S > (1LL << 31) - 1 || (long long)B * S * Hq > (1LL << 40) / d ||
+         (long long)B * (Hq + (long long)Hkv) > ((1LL << 31) - 1) / (4 * bwd_tiles(S));
+}
+
+}  // namespace
+}  // namespace fa
+
+extern "C" size_t fa_bwd_workspace_bytes(int B, int Hq, int Hkv, int S, int d, int causal) {
+  (void)causal;
+  if (!fa::bwd_sizes_ok(B, Hq, Hkv, S) || (d != 64 && d != 128) || fa::bwd_too_large(B, Hq, Hkv, S, d)) return 0;
+  return (size_t)B * Hq * fa::bwd_tiles(S) * fa::kStatBytes;
+}
+
+extern "C" fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                            const void* dout, const float* dlse, void* dq, void* dk, void* dv, int B, int Hq, int Hkv,
+                            int S, int d, int causal, float scale, void* workspace, size_t workspace_bytes,
+                            fa_stream_t stream) {
+  if (!q || !k || !v || !o || !lse || !dout || !dq || !dk || !dv) return FA_ERR_INVALID_ARG;
+  if (!fa::bwd_sizes_ok(B, Hq, Hkv, S) || !std::isfinite(scale) || scale <= 0.f) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (fa::bwd_too_large(B, Hq, Hkv, S, d)) return FA_ERR_UNSUPPORTED;
+  const void* bf16[] = {q, k, v, o, dout, dq, dk, dv};
+  for (const void* ptr : bf16)
+    if (!fa::is_aligned(ptr, 16)) return FA_ERR_ALIGNMENT;
+  if (!fa::is_aligned(lse, 4) || !fa::is_aligned(dlse, 4)) return FA_ERR_ALIGNMENT;
+  const uint64_t q_bytes = (uint64_t)B * S * Hq * d * 2, kv_bytes = (uint64_t)B * S * Hkv * d * 2;
+  const uint64_t l_bytes = (uint64_t)B * S * Hq * 4;
+  const size_t need = fa_bwd_workspace_bytes(B, Hq, Hkv, S, d, causal);
+  // every gradient is read and written by many CTAs at once: no output may share memory with
+  // another tensor of the call
+  const struct { const void* ptr; uint64_t bytes; } all[] = {
+      {dq, q_bytes}, {dk, kv_bytes}, {dv, kv_bytes}, {workspace, need}, {q, q_bytes}, {k, kv_bytes},
+      {v, kv_bytes}, {o, q_bytes}, {dout, q_bytes}, {lse, l_bytes}, {dlse, l_bytes}};
+  for (int i = 0; i < 4; ++i)
+    for (int j = i + 1; j < 11; ++j)
+      if (fa::overlaps(all[i].ptr, all[i].bytes, all[j].ptr, all[j].bytes)) return FA_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < need) return FA_ERR_WORKSPACE;
+  if (!fa::is_aligned(workspace, 256)) return FA_ERR_ALIGNMENT;
+  fa::DeviceStatus* status = nullptr;
+  int sm_count = 0;
+  const int rc = fa::current_device_info(&status, &sm_count);
+  if (rc != FA_OK) return (fa_status)rc;
+
+  fa::BwdParams p;
+  std::memset(&p, 0, sizeof(p));
+  const uint32_t box[4] = {64, 1, (uint32_t)fa::kTile, 1};
+  const uint64_t q_dims[4] = {(uint64_t)d, (uint64_t)Hq, (uint64_t)S, (uint64_t)B};
+  const uint64_t q_str[3] = {(uint64_t)d * 2, (uint64_t)Hq * d * 2, (uint64_t)S * Hq * d * 2};
+  const uint64_t k_dims[4] = {(uint64_t)d, (uint64_t)Hkv, (uint64_t)S, (uint64_t)B};
+  const uint64_t k_str[3] = {(uint64_t)d * 2, (uint64_t)Hkv * d * 2, (uint64_t)S * Hkv * d * 2};
+  if (!fa::make_bf16_map(&p.tm_q, q, q_dims, q_str, box) || !fa::make_bf16_map(&p.tm_do, dout, q_dims, q_str, box) ||
+      !fa::make_bf16_map(&p.tm_k, k, k_dims, k_str, box) || !fa::make_bf16_map(&p.tm_v, v, k_dims, k_str, box))
+    return FA_ERR_CUDA;
+  p.stat = static_cast<const float*>(workspace);
+  p.dq = static_cast<__nv_bfloat16*>(dq);
+  p.dk = static_cast<__nv_bfloat16*>(dk);
+  p.dv = static_cast<__nv_bfloat16*>(dv);
+  p.B = B;
+  p.S = S;
+  p.T = (int)fa::bwd_tiles(S);
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.group = Hq / Hkv;
+  p.causal = causal ? 1 : 0;
+  p.kv_units = p.T * B * Hkv;
+  auto chunk = [&](int heads) {
+    int c = (sm_count + p.T / 2) / p.T;
+    if (c < 1) c = 1;
+    return c < heads ? c : heads;
+  };
+  p.kv_chunk = chunk(B * Hkv);
+  p.q_chunk = chunk(B * Hq);
+  p.scale = scale;
+  p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  p.status = status;
+  fa::StatParams sp;
+  sp.o = static_cast<const __nv_bfloat16*>(o);
+  sp.dout = static_cast<const __nv_bfloat16*>(dout);
+  sp.lse = lse;
+  sp.dlse = dlse;
+  sp.stat = static_cast<float*>(workspace);
+  sp.B = B;
+  sp.S = S;
+  sp.T = p.T;
+  sp.Hq = Hq;
+  const int64_t units = (int64_t)p.T * B * ((int64_t)Hq + Hkv);
+  const cudaError_t e = d == 128 ? fa::launch_bwd<128>(sp, p, units, stream) : fa::launch_bwd<64>(sp, p, units, stream);
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
