@@ -17,7 +17,8 @@
 //
 // CTA organisation (384 threads, one CTA per SM):
 //   warp 0      TMA producer: the two resident tiles, then the streamed tiles into a ring of slots
-//   warp 1      TMEM owner; one lane issues every tcgen05.mma
+//   warp 1      TMEM owner; issues the MMAs of the scores and of what P (or, for dQ, dS) multiplies
+//   warp 2      issues the MMAs of dP and, for dK, of what dS multiplies
 //   warps 4-11  two warpgroups; thread t of a warpgroup owns row t of the 128 x 128 score tile
 //               (a TMEM lane), warpgroup g its columns [64 g, 64 g + 64)
 // P and dS are rounded to bf16 (the input type, as in the forward pass's P V) for their matrix
@@ -36,7 +37,7 @@ namespace {
 constexpr int kTile = 128;        // queries and keys per tile
 constexpr int kBwdThreads = 384;
 constexpr int kStatBytes = 1024;  // -LSE (base 2) and -delta of one query tile
-constexpr int kRegsBwdControl = 64;
+constexpr int kRegsBwdControl = 72;
 constexpr int kRegsBwdMath = 216;
 static_assert(128 * kRegsBwdControl + 256 * kRegsBwdMath <= kBwdThreads * 168, "register split too large");
 
@@ -162,273 +163,282 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, 
     tma_load_4d_hint(dst + sub * BwdCfg<D>::kSubBytes, map, bar, sub * 64, h, row, b, policy);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kBwdThreads, 1) bwd_kernel(const __grid_constant__ BwdParams p) {
-  using C = BwdCfg<D>;
-  constexpr int NS = C::kSlots;
-  constexpr int TB = C::kTileBytes;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  Ctl<D>& ctl = *reinterpret_cast<Ctl<D>*>(smem + C::kOffCtl);
-  static_assert(sizeof(Ctl<D>) <= 512, "control block too large");
-  uint8_t* slots = smem + 2 * TB;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  if (smem_u32(smem) & 1023u) {  // the swizzled tiles need 1024-byte alignment
-    if (threadIdx.x == 0 && atomicCAS(&p.status->code, 0u, 7u) == 0u) p.status->where = kSiteBwdSmem;
-    return;
-  }
-  if (threadIdx.x == 0) {
-    ctl.abort = 0;
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(&ctl.full[s], 1);
-      mbar_init(&ctl.empty[s], 1);
-    }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&ctl.s[s], 1);
-      mbar_init(&ctl.p[s], 8);  // two: a warp may reach step i + 1 before another has finished step i
-      mbar_init(&ctl.stat_full[s], 1);
-      mbar_init(&ctl.stat_empty[s], 8);  // one arrival per math warp
-    }
-    mbar_init(&ctl.resident, 1);
-    mbar_init(&ctl.dp, 1);
-    mbar_init(&ctl.ds, 8);
-    mbar_init(&ctl.acc, 1);
-    fence_mbar_init();
-  }
-  if (warp == 1) {
-    tmem_alloc(&ctl.tmem, 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = ctl.tmem;
-  volatile int* abort = &ctl.abort;
-  const BwdUnit u = bwd_unit(p);
+// What every role of a CTA needs to know of its unit; KEY is the kind of unit.
+template <int D, bool KEY>
+struct Layout {
   // TMEM columns: key unit: dV [0, D), dK [D, 2D), then score buffer 0, dP, score buffer 1;
   // query unit: dQ [0, D), then the same three tiles.
-  const uint32_t t_s0 = tmem + (u.key ? 2 * D : D);
-  const uint32_t t_dp = t_s0 + 128;
-  const int bufs = u.key ? C::kKeyScoreBufs : 2;
-  auto t_s = [&](int i) { return t_s0 + ((bufs == 2 && (i & 1)) ? 256u : 0u); };
-  auto s_bar = [&](int i) { return &ctl.s[bufs == 2 ? (i & 1) : 0]; };
-  auto s_par = [&](int i) { return (uint32_t)((bufs == 2 ? (i >> 1) : i) & 1); };
+  static constexpr int kBufs = KEY ? BwdCfg<D>::kKeyScoreBufs : 2;
+  static constexpr uint32_t kColS = KEY ? 2 * D : D;
+  static constexpr uint32_t kColDp = kColS + 128;
+  static_assert(kColS + 128 * (1 + kBufs) <= 512, "TMEM columns");
+  static __device__ __forceinline__ uint32_t col_s(int i) { return kColS + ((kBufs == 2 && (i & 1)) ? 256u : 0u); }
+  static __device__ __forceinline__ int s_bar(int i) { return kBufs == 2 ? (i & 1) : 0; }
+  static __device__ __forceinline__ uint32_t s_parity(int i) { return (uint32_t)((kBufs == 2 ? (i >> 1) : i) & 1); }
+};
 
-  if (warp == 0) {
-    regs_dec<kRegsBwdControl>();
-    // ================================================================ TMA producer
-    if (lane == 0) {
-      const uint64_t policy = policy_evict_last();  // every tile is read by many units
-      mbar_arrive_expect_tx(&ctl.resident, 2 * TB);
-      load_tile<D>(smem, u.key ? &p.tm_k : &p.tm_q, &ctl.resident, u.h, u.tile * kTile, u.b, policy);
-      load_tile<D>(smem + TB, u.key ? &p.tm_v : &p.tm_do, &ctl.resident, u.h, u.tile * kTile, u.b, policy);
-      // key unit: dO_i then Q_i (dO_i is released first); query unit: K_j then V_j
-      const CUtensorMap* map0 = u.key ? &p.tm_do : &p.tm_k;
-      const CUtensorMap* map1 = u.key ? &p.tm_q : &p.tm_v;
-      int it = 0, t = u.first, h = u.key ? u.h * p.group : u.h / p.group;
-      for (int i = 0; i < u.steps; ++i) {
+// TMA producer (one thread): the resident tiles, then the streamed ones. Key unit: dO_i then Q_i
+// (dO_i is released first) and the tile's statistics; query unit: K_j then V_j.
+template <int D, bool KEY>
+__device__ __forceinline__ void produce(const BwdParams& p, const BwdUnit& u, uint8_t* smem, Ctl<D>& ctl) {
+  using C = BwdCfg<D>;
+  constexpr int NS = C::kSlots, TB = C::kTileBytes;
+  volatile int* abort = &ctl.abort;
+  const uint64_t policy = policy_evict_last();  // every tile is read by many units
+  mbar_arrive_expect_tx(&ctl.resident, 2 * TB);
+  load_tile<D>(smem, KEY ? &p.tm_k : &p.tm_q, &ctl.resident, u.h, u.tile * kTile, u.b, policy);
+  load_tile<D>(smem + TB, KEY ? &p.tm_v : &p.tm_do, &ctl.resident, u.h, u.tile * kTile, u.b, policy);
+  uint8_t* slots = smem + 2 * TB;
+  int it = 0, t = u.first, h = KEY ? u.h * p.group : u.h / p.group;
+  for (int i = 0; i < u.steps; ++i) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half, ++it) {
-          const int s = it % NS;
-          if (it >= NS) mbar_wait(&ctl.empty[s], (it / NS + 1) & 1, abort, p.status, kSiteBwdEmpty);
-          mbar_arrive_expect_tx(&ctl.full[s], TB);
-          load_tile<D>(slots + s * TB, half ? map1 : map0, &ctl.full[s], h, t * kTile, u.b, policy);
-        }
-        if (u.key) {
-          if (i == 0) {  // the statistics come from the kernel before this one
-            griddep_wait();
-            asm volatile("fence.proxy.async.global;" ::: "memory");
-          }
-          const int s = i & 1;
-          if (i >= 2) mbar_wait(&ctl.stat_empty[s], (i / 2 + 1) & 1, abort, p.status, kSiteBwdStat);
-          mbar_arrive_expect_tx(&ctl.stat_full[s], kStatBytes);
-          bulk_load(smem + C::kOffStat + s * kStatBytes, p.stat + (((int64_t)u.b * p.Hq + h) * p.T + t) * 256,
-                    kStatBytes, &ctl.stat_full[s]);
-        }
-        if (++t == u.first + u.per) {
-          t = u.first;
-          ++h;
-        }
+    for (int half = 0; half < 2; ++half, ++it) {
+      const int s = it % NS;
+      if (it >= NS) mbar_wait(&ctl.empty[s], (it / NS + 1) & 1, abort, p.status, kSiteBwdEmpty);
+      mbar_arrive_expect_tx(&ctl.full[s], TB);
+      load_tile<D>(slots + s * TB, KEY ? (half ? &p.tm_q : &p.tm_do) : (half ? &p.tm_v : &p.tm_k), &ctl.full[s], h,
+                   t * kTile, u.b, policy);
+    }
+    if constexpr (KEY) {
+      if (i == 0) {  // the statistics come from the kernel before this one
+        griddep_wait();
+        asm volatile("fence.proxy.async.global;" ::: "memory");
       }
-      if (*abort) {  // after an abort nothing has waited for the copies in flight: do it here (bounded)
-        int no_abort = 0;
-        mbar_wait(&ctl.resident, 0, &no_abort, p.status, kSiteBwdDrain);
-        for (int k = it > NS ? it - NS : 0; k < it; ++k)
-          mbar_wait(&ctl.full[k % NS], (k / NS) & 1, &no_abort, p.status, kSiteBwdDrain);
-        if (u.key)
-          for (int k = u.steps > 2 ? u.steps - 2 : 0; k < u.steps; ++k)
-            mbar_wait(&ctl.stat_full[k & 1], (k / 2) & 1, &no_abort, p.status, kSiteBwdDrain);
-      }
+      const int s = i & 1;
+      if (i >= 2) mbar_wait(&ctl.stat_empty[s], (i / 2 + 1) & 1, abort, p.status, kSiteBwdStat);
+      mbar_arrive_expect_tx(&ctl.stat_full[s], kStatBytes);
+      bulk_load(smem + C::kOffStat + s * kStatBytes, p.stat + (((int64_t)u.b * p.Hq + h) * p.T + t) * 256, kStatBytes,
+                &ctl.stat_full[s]);
+    }
+    if (++t == u.first + u.per) {
+      t = u.first;
+      ++h;
+    }
+  }
+  if (*abort) {  // after an abort nothing has waited for the copies in flight: do it here (bounded)
+    int no_abort = 0;
+    mbar_wait(&ctl.resident, 0, &no_abort, p.status, kSiteBwdDrain);
+    for (int k = it > NS ? it - NS : 0; k < it; ++k)
+      mbar_wait(&ctl.full[k % NS], (k / NS) & 1, &no_abort, p.status, kSiteBwdDrain);
+    if (KEY)
+      for (int k = u.steps > 2 ? u.steps - 2 : 0; k < u.steps; ++k)
+        mbar_wait(&ctl.stat_full[k & 1], (k / 2) & 1, &no_abort, p.status, kSiteBwdDrain);
+  }
+}
+
+// MMA issuers: two warps, one per chain of dependences. Warp 1 (CHAIN 0) issues the scores and the
+// products of P (key unit) or of dS (query unit); warp 2 (CHAIN 1) issues dP and, in a key unit, the
+// products of dS. The whole warp runs the loop, so that slots and descriptors are computed in uniform
+// registers, and one elected lane issues each product: issued from a loop that only one lane runs,
+// every tcgen05.mma took about 100 cycles to issue (64 to execute), and the loop was bound by that.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
+}
+
+template <int D, bool KEY, int CHAIN>
+__device__ __forceinline__ void issue_mmas(const BwdParams& p, int n, uint8_t* smem, Ctl<D>& ctl, uint32_t tmem) {
+  using C = BwdCfg<D>;
+  using L = Layout<D, KEY>;
+  constexpr int NS = C::kSlots, TB = C::kTileBytes;
+  volatile int* abort = &ctl.abort;
+  const uint64_t a = make_sdesc_sw128(smem_u32(smem) + CHAIN * TB, 16, 1024);         // this chain's resident tile
+  const uint64_t bk = make_sdesc_sw128(smem_u32(smem + 2 * TB), 16, 1024);            // K-major view of slot 0
+  const uint64_t bm = make_sdesc_sw128(smem_u32(smem + 2 * TB), C::kSubBytes, 1024);  // MN-major view of slot 0
+  auto wait_full = [&](int it) { mbar_wait(&ctl.full[it % NS], (it / NS) & 1, abort, p.status, kSiteBwdFull); };
+  auto slot = [&](int it) { return (uint64_t)((it % NS) * (TB >> 4)); };
+  // streamed items: key unit dO_i = 2 i, Q_i = 2 i + 1; query unit K_j = 2 j, V_j = 2 j + 1
+  constexpr int kScoreItem = KEY ? 1 : 0;  // S^T = K Q_i^T, S = Q K_j^T
+  constexpr int kProbItem = KEY ? 0 : 1;   // dP^T = V dO_i^T, dP = dO V_j^T
+  auto scores = [&](int i) {
+    const int it = 2 * i + kScoreItem;
+    wait_full(it);
+    __syncwarp();
+    tc_fence_after();
+    if (elect_one()) {
+      mma_scores<D>(tmem + L::col_s(i), a, bk + slot(it));
+      mma_commit(&ctl.s[L::s_bar(i)]);
+      if (KEY) mma_commit(&ctl.empty[it % NS]);  // with the other chain's arrival, Q_i is released
     }
     __syncwarp();
-  } else if (warp == 1) {
-    regs_dec<kRegsBwdControl>();
-    // ================================================================ MMA issuer
-    if (lane == 0) {
-      const uint64_t a0 = make_sdesc_sw128(smem_u32(smem), 16, 1024);
-      const uint64_t a1 = a0 + (TB >> 4);
-      const uint64_t bk = make_sdesc_sw128(smem_u32(slots), 16, 1024);              // K-major view of slot 0
-      const uint64_t bm = make_sdesc_sw128(smem_u32(slots), C::kSubBytes, 1024);    // MN-major view of slot 0
-      const int n = u.steps;
-      auto wait_full = [&](int it) {
-        mbar_wait(&ctl.full[it % NS], (it / NS) & 1, abort, p.status, kSiteBwdFull);
-        tc_fence_after();
-      };
-      auto slot = [&](int it) { return (uint64_t)((it % NS) * (TB >> 4)); };
-      mbar_wait(&ctl.resident, 0, abort, p.status, kSiteBwdResident);
-      if (u.key) {
-        auto scores = [&](int i) {  // S^T = K Q_i^T
-          wait_full(2 * i + 1);
-          mma_scores<D>(t_s(i), a0, bk + slot(2 * i + 1));
-          mma_commit(s_bar(i));
-        };
-        auto dprob = [&](int i) {  // dP^T = V dO_i^T
-          wait_full(2 * i);
-          mma_scores<D>(t_dp, a1, bk + slot(2 * i));
-          mma_commit(&ctl.dp);
-        };
-        scores(0);
-        dprob(0);
-        if (bufs == 2 && n > 1) scores(1);
-        for (int i = 0; i < n; ++i) {
-          mbar_wait(&ctl.p[i & 1], (i >> 1) & 1, abort, p.status, kSiteBwdP);
-          tc_fence_after();
-          mma_accumulate<D>(tmem, t_s(i), bm + slot(2 * i), i > 0);  // dV += P^T dO_i
-          mma_commit(&ctl.empty[(2 * i) % NS]);
-          if (i + bufs < n) scores(i + bufs);  // into the buffer P_i leaves
-          mbar_wait(&ctl.ds, i & 1, abort, p.status, kSiteBwdDs);
-          tc_fence_after();
-          mma_accumulate<D>(tmem + D, t_dp, bm + slot(2 * i + 1), i > 0);  // dK += dS^T Q_i
-          mma_commit(&ctl.empty[(2 * i + 1) % NS]);
-          if (i + 1 < n) dprob(i + 1);
-        }
+  };
+  auto dprob = [&](int i) {
+    const int it = 2 * i + kProbItem;
+    wait_full(it);
+    __syncwarp();
+    tc_fence_after();
+    if (elect_one()) {
+      mma_scores<D>(tmem + L::kColDp, a, bk + slot(it));
+      mma_commit(&ctl.dp);
+      mma_commit(&ctl.empty[it % NS]);
+    }
+    __syncwarp();
+  };
+  mbar_wait(&ctl.resident, 0, abort, p.status, kSiteBwdResident);
+  if constexpr (CHAIN == 0) {
+    scores(0);
+    if (L::kBufs == 2 && n > 1) scores(1);
+    for (int i = 0; i < n; ++i) {
+      const int it = 2 * i;  // dO_i, or K_j
+      if (KEY) {
+        wait_full(it);
+        mbar_wait(&ctl.p[i & 1], (i >> 1) & 1, abort, p.status, kSiteBwdP);
       } else {
-        auto scores = [&](int j) {  // S = Q K_j^T
-          wait_full(2 * j);
-          mma_scores<D>(t_s(j), a0, bk + slot(2 * j));
-          mma_commit(s_bar(j));
-        };
-        auto dprob = [&](int j) {  // dP = dO V_j^T, after which V_j is done with
-          wait_full(2 * j + 1);
-          mma_scores<D>(t_dp, a1, bk + slot(2 * j + 1));
-          mma_commit(&ctl.dp);
-          mma_commit(&ctl.empty[(2 * j + 1) % NS]);
-        };
-        scores(0);
-        dprob(0);
-        if (n > 1) scores(1);
-        for (int j = 0; j < n; ++j) {
-          // dS_j is written (over S_j), and dP_j has been read: dP_{j+1} goes first, because the
-          // math warps need it next
-          mbar_wait(&ctl.ds, j & 1, abort, p.status, kSiteBwdDs);
-          tc_fence_after();
-          if (j + 1 < n) dprob(j + 1);
-          mma_accumulate<D>(tmem, t_s(j), bm + slot(2 * j), j > 0);  // dQ += dS K_j
-          mma_commit(&ctl.empty[(2 * j) % NS]);
-          if (j + 2 < n) scores(j + 2);
-        }
+        mbar_wait(&ctl.ds, i & 1, abort, p.status, kSiteBwdDs);
       }
-      // every MMA has completed before TMEM is released
-      mma_commit(&ctl.acc);
-      int no_abort = 0;
-      mbar_wait(&ctl.acc, 0, &no_abort, p.status, kSiteBwdDrain);
-    }
-    __syncwarp();
-  } else if (warp >= 4) {
-    regs_inc<kRegsBwdMath>();
-    // ================================================================ P, dS and the epilogue
-    const int g = (warp - 4) >> 2;
-    const int row = (warp & 3) * 32 + lane;
-    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t half_off = lane_off + 64 * g;
-    const uint64_t c2 = f32x2(p.scale_log2, p.scale_log2);
-    // query unit: this row's statistics
-    float nlse = 0.f, ndelta = 0.f;
-    if (!u.key) {
-      griddep_wait();
-      const float* st = p.stat + (((int64_t)u.b * p.Hq + u.h) * p.T + u.tile) * 256;
-      nlse = st[row];
-      ndelta = st[128 + row];
-    }
-    int t = u.first;
-    for (int i = 0; i < u.steps; ++i) {
-      // columns [lo, hi) of this row's 64 are not masked
-      int lo = 0, hi = 64;
-      if (p.causal && t == u.tile) {
-        if (u.key) lo = row - 64 * g;
-        else hi = row + 1 - 64 * g;
-      }
-      if (!u.key && (t + 1) * kTile > p.S) hi = min(hi, p.S - t * kTile - 64 * g);
-      const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < 64);
-      const float* st = reinterpret_cast<const float*>(smem + C::kOffStat + (i & 1) * kStatBytes) + 64 * g;
-      if (u.key) mbar_wait(&ctl.stat_full[i & 1], (i >> 1) & 1, abort, p.status, kSiteBwdStat);
-      mbar_wait(s_bar(i), s_par(i), abort, p.status, kSiteBwdS);
       __syncwarp();
       tc_fence_after();
-      uint64_t pr[32];  // P of this row's 64 columns, in pairs
-      const uint32_t ts = t_s(i) + half_off;
-#pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
-        uint32_t sr[32];
-        tmem_ld32(ts + 32 * cc, sr);
-        tmem_ld_wait(sr);
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          uint64_t nl;
-          if (u.key) nl = *reinterpret_cast<const uint64_t*>(st + 32 * cc + 2 * k);
-          else nl = f32x2(nlse, nlse);
-          float x0, x1;
-          split_f32x2(fma_f32x2(f32x2(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1])), c2, nl), x0, x1);
-          pr[16 * cc + k] = f32x2(ex2(x0), ex2(x1));
-        }
+      if (elect_one()) {
+        mma_accumulate<D>(tmem, tmem + L::col_s(i), bm + slot(it), i > 0);  // dV += P^T dO_i, dQ += dS K_j
+        mma_commit(&ctl.empty[it % NS]);
       }
-      if (masked) {
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          float a, b;
-          split_f32x2(pr[k], a, b);
-          if (2 * k < lo || 2 * k >= hi) a = 0.f;
-          if (2 * k + 1 < lo || 2 * k + 1 >= hi) b = 0.f;
-          pr[k] = f32x2(a, b);
-        }
-      }
-      if (u.key) {  // P^T is dV's A operand, written over this half's scores
-#pragma unroll
-        for (int cc = 0; cc < 2; ++cc) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float a, b;
-            split_f32x2(pr[16 * cc + k], a, b);
-            pk[k] = pack_bf16x2(a, b);
-          }
-          tmem_st16(ts + 16 * cc, pk);
-        }
-        tmem_st_wait();
-        tc_fence_before();
+      __syncwarp();
+      if (i + L::kBufs < n) scores(i + L::kBufs);  // into the buffer that P_i, or dS_j, leaves
+    }
+  } else {
+    dprob(0);
+    for (int i = 0; i < n; ++i) {
+      if (!KEY && i + 1 == n) break;
+      mbar_wait(&ctl.ds, i & 1, abort, p.status, kSiteBwdDs);  // dS_i is written, and dP_i has been read
+      if (KEY) {
+        const int it = 2 * i + 1;
+        wait_full(it);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.p[i & 1]);
+        tc_fence_after();
+        if (elect_one()) {
+          mma_accumulate<D>(tmem + D, tmem + L::kColDp, bm + slot(it), i > 0);  // dK += dS^T Q_i
+          mma_commit(&ctl.empty[it % NS]);
+        }
+        __syncwarp();
       }
-      mbar_wait(&ctl.dp, i & 1, abort, p.status, kSiteBwdDp);
-      __syncwarp();
-      tc_fence_after();
-      const uint32_t td = t_dp + half_off;
-      const uint32_t t_out = u.key ? td : ts;  // dS goes over dP (key unit) or over the scores
+      if (i + 1 < n) dprob(i + 1);
+    }
+  }
+  // every MMA has completed before TMEM is released (the barrier counts both chains)
+  __syncwarp();
+  if (elect_one()) mma_commit(&ctl.acc);
+  __syncwarp();
+  int no_abort = 0;
+  mbar_wait(&ctl.acc, 0, &no_abort, p.status, kSiteBwdDrain);
+}
+
+// P and dS of one row's 64 columns per step, then the gradients' epilogue.
+template <int D, bool KEY>
+__device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u, uint8_t* smem, Ctl<D>& ctl,
+                                           uint32_t tmem) {
+  using C = BwdCfg<D>;
+  using L = Layout<D, KEY>;
+  volatile int* abort = &ctl.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = (warp - 4) >> 2;
+  const int row = (warp & 3) * 32 + lane;
+  const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+  const uint32_t half_off = lane_off + 64 * g;
+  const uint64_t c2 = f32x2(p.scale_log2, p.scale_log2);
+  uint64_t nlse2 = 0, ndelta2 = 0;  // query unit: this row's statistics
+  if constexpr (!KEY) {
+    griddep_wait();
+    const float* st = p.stat + (((int64_t)u.b * p.Hq + u.h) * p.T + u.tile) * 256;
+    nlse2 = f32x2(st[row], st[row]);
+    ndelta2 = f32x2(st[128 + row], st[128 + row]);
+  }
+  int t = u.first;
+  for (int i = 0; i < u.steps; ++i) {
+    // columns [lo, hi) of this row's 64 are not masked
+    int lo = 0, hi = 64;
+    if (p.causal && t == u.tile) {
+      if (KEY) lo = row - 64 * g;
+      else hi = row + 1 - 64 * g;
+    }
+    if (!KEY && (t + 1) * kTile > p.S) hi = min(hi, p.S - t * kTile - 64 * g);
+    const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < 64);
+    // key unit: the statistics of the columns (every lane reads the same 16 bytes)
+    const ulonglong2* st =
+        reinterpret_cast<const ulonglong2*>(smem + C::kOffStat + (i & 1) * kStatBytes + 64 * g * sizeof(float));
+    if (KEY) mbar_wait(&ctl.stat_full[i & 1], (i >> 1) & 1, abort, p.status, kSiteBwdStat);
+    mbar_wait(&ctl.s[L::s_bar(i)], L::s_parity(i), abort, p.status, kSiteBwdS);
+    __syncwarp();
+    tc_fence_after();
+    uint64_t pr[32];  // P of this row's 64 columns, in pairs
+    const uint32_t ts = tmem + L::col_s(i) + half_off;
+    {
+      uint32_t sr[64];
+      tmem_ld32(ts, sr);
+      tmem_ld32(ts + 32, sr + 32);
+      tmem_ld_wait(sr);
+      tmem_ld_wait(sr + 32);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        ulonglong2 nl;
+        if constexpr (KEY) nl = st[k];
+        else nl = make_ulonglong2(nlse2, nlse2);
+        float x0, x1, x2, x3;
+        split_f32x2(fma_f32x2(f32x2(__uint_as_float(sr[4 * k]), __uint_as_float(sr[4 * k + 1])), c2, nl.x), x0, x1);
+        split_f32x2(fma_f32x2(f32x2(__uint_as_float(sr[4 * k + 2]), __uint_as_float(sr[4 * k + 3])), c2, nl.y), x2, x3);
+        pr[2 * k] = f32x2(ex2(x0), ex2(x1));
+        pr[2 * k + 1] = f32x2(ex2(x2), ex2(x3));
+      }
+    }
+    if (masked) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        float a, b;
+        split_f32x2(pr[k], a, b);
+        if (2 * k < lo || 2 * k >= hi) a = 0.f;
+        if (2 * k + 1 < lo || 2 * k + 1 >= hi) b = 0.f;
+        pr[k] = f32x2(a, b);
+      }
+    }
+    if constexpr (KEY) {  // P^T is dV's A operand, written over this half's scores
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) {
-        uint32_t dr[32], pk[16];
-        tmem_ld32(td + 32 * cc, dr);
-        tmem_ld_wait(dr);
+        uint32_t pk[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          uint64_t nd;
-          if (u.key) nd = *reinterpret_cast<const uint64_t*>(st + 128 + 32 * cc + 2 * k);
-          else nd = f32x2(ndelta, ndelta);
-          const uint64_t v = mul_f32x2(
-              pr[16 * cc + k], add_f32x2(f32x2(__uint_as_float(dr[2 * k]), __uint_as_float(dr[2 * k + 1])), nd));
           float a, b;
-          split_f32x2(v, a, b);
+          split_f32x2(pr[16 * cc + k], a, b);
           pk[k] = pack_bf16x2(a, b);
+        }
+        tmem_st16(ts + 16 * cc, pk);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.p[i & 1]);
+    }
+    mbar_wait(&ctl.dp, i & 1, abort, p.status, kSiteBwdDp);
+    __syncwarp();
+    tc_fence_after();
+    const uint32_t td = tmem + L::kColDp + half_off;
+    const uint32_t t_out = KEY ? td : ts;  // dS goes over dP (key unit) or over the scores
+    {
+      uint32_t dr[64];
+      tmem_ld32(td, dr);
+      tmem_ld32(td + 32, dr + 32);
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        uint32_t pk[16];
+        tmem_ld_wait(dr + 32 * cc);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          ulonglong2 nd;
+          if constexpr (KEY) nd = st[32 + 8 * cc + k];
+          else nd = make_ulonglong2(ndelta2, ndelta2);
+          const uint32_t* d4 = dr + 32 * cc + 4 * k;
+          const uint64_t v0 = mul_f32x2(pr[16 * cc + 2 * k],
+                                        add_f32x2(f32x2(__uint_as_float(d4[0]), __uint_as_float(d4[1])), nd.x));
+          const uint64_t v1 = mul_f32x2(pr[16 * cc + 2 * k + 1],
+                                        add_f32x2(f32x2(__uint_as_float(d4[2]), __uint_as_float(d4[3])), nd.y));
+          float a, b;
+          split_f32x2(v0, a, b);
+          pk[2 * k] = pack_bf16x2(a, b);
+          split_f32x2(v1, a, b);
+          pk[2 * k + 1] = pack_bf16x2(a, b);
         }
         if (masked) {  // not 0 times dP: dP may be infinite or NaN where masked
 #pragma unroll
@@ -440,47 +450,104 @@ __global__ void __launch_bounds__(kBwdThreads, 1) bwd_kernel(const __grid_consta
         }
         tmem_st16(t_out + 16 * cc, pk);
       }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&ctl.ds);
-        if (u.key) mbar_arrive(&ctl.stat_empty[i & 1]);
-      }
-      if (++t == u.first + u.per) t = u.first;
     }
-    // ------------------------------------------------------------ epilogue
-    mbar_wait(&ctl.acc, 0, abort, p.status, kSiteBwdAcc);
+    tmem_st_wait();
+    tc_fence_before();
     __syncwarp();
-    tc_fence_after();
-    // key unit: warpgroup 0 stores dV, warpgroup 1 dK; query unit: half of dQ's columns each
-    const int cols = u.key ? D : D / 2;
-    const uint32_t tacc = tmem + lane_off + g * cols;
-    const int heads = u.key ? p.Hkv : p.Hq;
-    const int srow = u.tile * kTile + row;
-    __nv_bfloat16* base = u.key ? (g == 0 ? p.dv : p.dk) : p.dq + g * cols;
-    base += (((int64_t)u.b * p.S + srow) * heads + u.h) * D;
-    const float mul = (u.key && g == 0) ? 1.f : p.scale;
-    const bool store = srow < p.S;
+    if (lane == 0) {
+      mbar_arrive(&ctl.ds);
+      if (KEY) mbar_arrive(&ctl.stat_empty[i & 1]);
+    }
+    if (++t == u.first + u.per) t = u.first;
+  }
+  // ------------------------------------------------------------ epilogue
+  mbar_wait(&ctl.acc, 0, abort, p.status, kSiteBwdAcc);
+  __syncwarp();
+  tc_fence_after();
+  // key unit: warpgroup 0 stores dV, warpgroup 1 dK; query unit: half of dQ's columns each
+  constexpr int kCols = KEY ? D : D / 2;
+  const uint32_t tacc = tmem + lane_off + g * kCols;
+  const int heads = KEY ? p.Hkv : p.Hq;
+  const int srow = u.tile * kTile + row;
+  __nv_bfloat16* base = KEY ? (g == 0 ? p.dv : p.dk) : p.dq + g * kCols;
+  base += (((int64_t)u.b * p.S + srow) * heads + u.h) * D;
+  const float mul = (KEY && g == 0) ? 1.f : p.scale;
 #pragma unroll 1
-    for (int cc = 0; cc < cols / 32; ++cc) {
-      uint32_t r[32];
-      tmem_ld32(tacc + 32 * cc, r);
-      tmem_ld_wait(r);
-      if (store) {
-        uint4* dst = reinterpret_cast<uint4*>(base + 32 * cc);
+  for (int cc = 0; cc < kCols / 32; ++cc) {
+    uint32_t r[32];
+    tmem_ld32(tacc + 32 * cc, r);
+    tmem_ld_wait(r);
+    if (srow < p.S) {
+      uint4* dst = reinterpret_cast<uint4*>(base + 32 * cc);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t w[4];
+      for (int k = 0; k < 4; ++k) {
+        uint32_t w[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            w[x] = pack_bf16x2(__uint_as_float(r[8 * k + 2 * x]) * mul, __uint_as_float(r[8 * k + 2 * x + 1]) * mul);
-          dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        for (int x = 0; x < 4; ++x)
+          w[x] = pack_bf16x2(__uint_as_float(r[8 * k + 2 * x]) * mul, __uint_as_float(r[8 * k + 2 * x + 1]) * mul);
+        dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kBwdThreads, 1) bwd_kernel(const __grid_constant__ BwdParams p) {
+  using C = BwdCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Ctl<D>& ctl = *reinterpret_cast<Ctl<D>*>(smem + C::kOffCtl);
+  static_assert(sizeof(Ctl<D>) <= 512, "control block too large");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (smem_u32(smem) & 1023u) {  // the swizzled tiles need 1024-byte alignment
+    if (threadIdx.x == 0 && atomicCAS(&p.status->code, 0u, 7u) == 0u) p.status->where = kSiteBwdSmem;
+    return;
+  }
+  const BwdUnit u = bwd_unit(p);
+  if (threadIdx.x == 0) {
+    ctl.abort = 0;
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(&ctl.full[s], 1);
+      mbar_init(&ctl.empty[s], u.key ? 2 : 1);  // products that read the tile: both chains, or one
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctl.s[s], 1);
+      mbar_init(&ctl.p[s], 8);  // two: a warp may reach step i + 1 before another has finished step i
+      mbar_init(&ctl.stat_full[s], 1);
+      mbar_init(&ctl.stat_empty[s], 8);  // one arrival per math warp
+    }
+    mbar_init(&ctl.resident, 1);
+    mbar_init(&ctl.dp, 1);
+    mbar_init(&ctl.ds, 8);
+    mbar_init(&ctl.acc, 2);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctl.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem;
+
+  if (warp >= 4) {
+    regs_inc<kRegsBwdMath>();
+    if (u.key) math_warps<D, true>(p, u, smem, ctl, tmem);
+    else math_warps<D, false>(p, u, smem, ctl, tmem);
   } else {
     regs_dec<kRegsBwdControl>();
+    if (warp == 0 && lane == 0) {
+      if (u.key) produce<D, true>(p, u, smem, ctl);
+      else produce<D, false>(p, u, smem, ctl);
+    } else if (warp == 1) {
+      if (u.key) issue_mmas<D, true, 0>(p, u.steps, smem, ctl, tmem);
+      else issue_mmas<D, false, 0>(p, u.steps, smem, ctl, tmem);
+    } else if (warp == 2) {
+      if (u.key) issue_mmas<D, true, 1>(p, u.steps, smem, ctl, tmem);
+      else issue_mmas<D, false, 1>(p, u.steps, smem, ctl, tmem);
+    }
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
