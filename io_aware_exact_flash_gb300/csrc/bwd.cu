@@ -37,8 +37,8 @@ namespace {
 constexpr int kTile = 128;        // queries and keys per tile
 constexpr int kBwdThreads = 384;
 constexpr int kStatBytes = 1024;  // -LSE (base 2) and -delta of one query tile
-constexpr int kRegsBwdControl = 72;
-constexpr int kRegsBwdMath = 216;
+constexpr int kRegsBwdControl = 88;
+constexpr int kRegsBwdMath = 208;
 static_assert(128 * kRegsBwdControl + 256 * kRegsBwdMath <= kBwdThreads * 168, "register split too large");
 
 enum : uint32_t {
@@ -53,6 +53,9 @@ enum : uint32_t {
   kSiteBwdAcc = 38,
   kSiteBwdDrain = 39,
   kSiteBwdSmem = 40,
+  kSiteBwdTurn = 41,
+  kSiteBwdTake = 42,
+  kSiteBwdAccFree = 43,
 };
 
 struct alignas(64) BwdParams {
@@ -84,18 +87,28 @@ struct BwdCfg {
   static constexpr int kKeyScoreBufs = D == 128 ? 1 : 2;
   static constexpr int kOffStat = (2 + kSlots) * kTileBytes;
   static constexpr int kOffCtl = kOffStat + 2 * kStatBytes;
-  static constexpr int kSmemBytes = kOffCtl + 512;
+  static constexpr int kCtlBytes = 768;
+  static constexpr int kSmemBytes = kOffCtl + kCtlBytes;
 };
 
 // Barriers and flags at the end of the CTA's shared memory (no static shared memory: the tiles at
-// its start must be 1024-byte aligned and leave no room for padding at d = 128).
+// its start must be 1024-byte aligned and leave no room for padding at d = 128). A CTA runs units of
+// both kinds one after the other; what counts steps has a set of barriers for each kind.
+template <int D>
+struct StepBars {
+  uint64_t full[BwdCfg<D>::kSlots], empty[BwdCfg<D>::kSlots];
+  uint64_t s[2], dp, p[2], ds, turn[2], stat_full[2], stat_empty[2];
+};
 template <int D>
 struct Ctl {
-  uint64_t full[BwdCfg<D>::kSlots], empty[BwdCfg<D>::kSlots];
-  uint64_t resident, s[2], dp, p[2], ds, acc, stat_full[2], stat_empty[2];
+  uint4 resp[2];                           // launch cancellation responses
+  uint64_t resp_full[2], resp_empty[2];
+  StepBars<D> kind[2];                     // query units, key units
+  uint64_t resident, acc, acc_free;        // one phase per unit
   uint32_t tmem;
   int abort;
 };
+constexpr int kBwdWalkers = 11;  // warps that walk the units: 0 to 2 and 4 to 11
 
 // Which tiles a CTA owns and streams.
 struct BwdUnit {
@@ -108,9 +121,9 @@ struct BwdUnit {
 // Units are ordered by chunks of heads, about one wave of CTAs per chunk, so that CTAs running
 // together stream the same few heads' tiles from L2; inside a chunk the units with the most steps
 // come first. Key units precede query units: they are the long ones when heads share keys.
-__device__ __forceinline__ BwdUnit bwd_unit(const BwdParams& p) {
+__device__ __forceinline__ BwdUnit bwd_unit(const BwdParams& p, int index) {
   BwdUnit u;
-  int r = blockIdx.x;
+  int r = index;
   u.key = r < p.kv_units;
   if (!u.key) r -= p.kv_units;
   const int heads = u.key ? p.Hkv : p.Hq;
@@ -155,6 +168,12 @@ __device__ __forceinline__ void mma_accumulate(uint32_t acc, uint32_t a_tmem, ui
            (kk > 0 || accumulate) ? 1u : 0u);
 }
 
+__device__ __forceinline__ void st_global_32(void* dst, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 template <int D>
 __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int h, int row, int b,
                                           uint64_t policy) {
@@ -173,64 +192,29 @@ struct Layout {
   static constexpr uint32_t kColDp = kColS + 128;
   static_assert(kColS + 128 * (1 + kBufs) <= 512, "TMEM columns");
   static __device__ __forceinline__ uint32_t col_s(int i) { return kColS + ((kBufs == 2 && (i & 1)) ? 256u : 0u); }
+  // Slots of the streamed tiles. Key unit: one ring, dO_i then Q_i (dO_i is released first). Query
+  // unit: a ring for K (held until dQ's product) and one for V (released by dP): in a common ring V_j
+  // waited for the slot of K_{j-2}, whose release left too little time for the load.
+  static constexpr int kFirst = KEY ? BwdCfg<D>::kSlots : (BwdCfg<D>::kSlots + 1) / 2;  // slots of ring 0
+  struct Slot {
+    int slot;
+    uint32_t fill;  // how often the slot has been filled before
+  };
+  static __device__ __forceinline__ Slot slot_of(int i, int which) {  // which: 0 dO / K, 1 Q / V
+    if constexpr (KEY) {
+      const int it = 2 * i + which;
+      return {it % kFirst, (uint32_t)(it / kFirst)};
+    } else if (which == 0) {
+      return {i % kFirst, (uint32_t)(i / kFirst)};
+    } else {
+      constexpr int n = BwdCfg<D>::kSlots - kFirst;
+      return {kFirst + i % n, (uint32_t)(i / n)};
+    }
+  }
   static __device__ __forceinline__ int s_bar(int i) { return kBufs == 2 ? (i & 1) : 0; }
   static __device__ __forceinline__ uint32_t s_parity(int i) { return (uint32_t)((kBufs == 2 ? (i >> 1) : i) & 1); }
 };
 
-// TMA producer (one thread): the resident tiles, then the streamed ones. Key unit: dO_i then Q_i
-// (dO_i is released first) and the tile's statistics; query unit: K_j then V_j.
-template <int D, bool KEY>
-__device__ __forceinline__ void produce(const BwdParams& p, const BwdUnit& u, uint8_t* smem, Ctl<D>& ctl) {
-  using C = BwdCfg<D>;
-  constexpr int NS = C::kSlots, TB = C::kTileBytes;
-  volatile int* abort = &ctl.abort;
-  const uint64_t policy = policy_evict_last();  // every tile is read by many units
-  mbar_arrive_expect_tx(&ctl.resident, 2 * TB);
-  load_tile<D>(smem, KEY ? &p.tm_k : &p.tm_q, &ctl.resident, u.h, u.tile * kTile, u.b, policy);
-  load_tile<D>(smem + TB, KEY ? &p.tm_v : &p.tm_do, &ctl.resident, u.h, u.tile * kTile, u.b, policy);
-  uint8_t* slots = smem + 2 * TB;
-  int it = 0, t = u.first, h = KEY ? u.h * p.group : u.h / p.group;
-  for (int i = 0; i < u.steps; ++i) {
-#pragma unroll
-    for (int half = 0; half < 2; ++half, ++it) {
-      const int s = it % NS;
-      if (it >= NS) mbar_wait(&ctl.empty[s], (it / NS + 1) & 1, abort, p.status, kSiteBwdEmpty);
-      mbar_arrive_expect_tx(&ctl.full[s], TB);
-      load_tile<D>(slots + s * TB, KEY ? (half ? &p.tm_q : &p.tm_do) : (half ? &p.tm_v : &p.tm_k), &ctl.full[s], h,
-                   t * kTile, u.b, policy);
-    }
-    if constexpr (KEY) {
-      if (i == 0) {  // the statistics come from the kernel before this one
-        griddep_wait();
-        asm volatile("fence.proxy.async.global;" ::: "memory");
-      }
-      const int s = i & 1;
-      if (i >= 2) mbar_wait(&ctl.stat_empty[s], (i / 2 + 1) & 1, abort, p.status, kSiteBwdStat);
-      mbar_arrive_expect_tx(&ctl.stat_full[s], kStatBytes);
-      bulk_load(smem + C::kOffStat + s * kStatBytes, p.stat + (((int64_t)u.b * p.Hq + h) * p.T + t) * 256, kStatBytes,
-                &ctl.stat_full[s]);
-    }
-    if (++t == u.first + u.per) {
-      t = u.first;
-      ++h;
-    }
-  }
-  if (*abort) {  // after an abort nothing has waited for the copies in flight: do it here (bounded)
-    int no_abort = 0;
-    mbar_wait(&ctl.resident, 0, &no_abort, p.status, kSiteBwdDrain);
-    for (int k = it > NS ? it - NS : 0; k < it; ++k)
-      mbar_wait(&ctl.full[k % NS], (k / NS) & 1, &no_abort, p.status, kSiteBwdDrain);
-    if (KEY)
-      for (int k = u.steps > 2 ? u.steps - 2 : 0; k < u.steps; ++k)
-        mbar_wait(&ctl.stat_full[k & 1], (k / 2) & 1, &no_abort, p.status, kSiteBwdDrain);
-  }
-}
-
-// MMA issuers: two warps, one per chain of dependences. Warp 1 (CHAIN 0) issues the scores and the
-// products of P (key unit) or of dS (query unit); warp 2 (CHAIN 1) issues dP and, in a key unit, the
-// products of dS. The whole warp runs the loop, so that slots and descriptors are computed in uniform
-// registers, and one elected lane issues each product: issued from a loop that only one lane runs,
-// every tcgen05.mma took about 100 cycles to issue (64 to execute), and the loop was bound by that.
 __device__ __forceinline__ bool elect_one() {
   uint32_t e;
   asm volatile(
@@ -241,99 +225,235 @@ __device__ __forceinline__ bool elect_one() {
   return e != 0;
 }
 
-template <int D, bool KEY, int CHAIN>
-__device__ __forceinline__ void issue_mmas(const BwdParams& p, int n, uint8_t* smem, Ctl<D>& ctl, uint32_t tmem) {
+// A CTA runs unit blockIdx.x, then takes over the units of CTAs that have not started (cluster launch
+// control), so that set-up is paid once per SM and the next unit's loads overlap the last one's end.
+// The producer asks once it has issued a unit's loads; every walker reads the response. Returns the
+// r-th taken unit (r counts from 0), or -1 when there is none left.
+template <int D>
+__device__ __forceinline__ int taken_unit(const BwdParams& p, Ctl<D>& ctl, int r) {
+  int index = -1;
+  if (mbar_wait(&ctl.resp_full[r & 1], (r >> 1) & 1, &ctl.abort, p.status, kSiteBwdTake))
+    index = launch_cancel_result(&ctl.resp[r & 1]);
+  index = __shfl_sync(0xffffffffu, index, 0);
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&ctl.resp_empty[r & 1]);
+  return index;
+}
+
+// The last copy issued into each slot (bit 16 kind + slot), statistics buffer (after the slots),
+// the resident tiles and the two response slots, with its barrier's phase.
+struct Copies {
+  static constexpr int kResident = 12, kResponse = 13;
+  uint32_t issued = 0, parity = 0;
+  __device__ __forceinline__ void note(int bit, int phase) {
+    issued |= 1u << bit;
+    parity = (parity & ~(1u << bit)) | ((uint32_t)(phase & 1) << bit);
+  }
+};
+
+// TMA producer (lane 0 of its warp): the streamed tiles and, once the previous unit's products are
+// done, the resident ones. Key unit: dO_i, Q_i and the tile's statistics; query unit: K_j and V_j.
+// r: units this CTA has run before; first: steps it has run in units of this kind; same: the previous
+// unit was of this kind too (its slots are then released one by one).
+template <int D, bool KEY>
+__device__ __forceinline__ void produce(const BwdParams& p, const BwdUnit& u, uint8_t* smem, Ctl<D>& ctl, int r,
+                                        int first, bool same, Copies& copies) {
   using C = BwdCfg<D>;
   using L = Layout<D, KEY>;
-  constexpr int NS = C::kSlots, TB = C::kTileBytes;
+  constexpr int TB = C::kTileBytes;
+  StepBars<D>& bars = ctl.kind[KEY];
   volatile int* abort = &ctl.abort;
+  const uint64_t policy = policy_evict_last();  // every tile is read by many units
+  uint8_t* slots = smem + 2 * TB;
+  if (r > 0 && !same) mbar_wait(&ctl.acc, (r - 1) & 1, abort, p.status, kSiteBwdAcc);
+  int t = u.first, h = KEY ? u.h * p.group : u.h / p.group;
+  for (int i = 0; i < u.steps; ++i) {
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const auto f = L::slot_of(first + i, which);
+      if (f.fill > 0) mbar_wait(&bars.empty[f.slot], (f.fill + 1) & 1, abort, p.status, kSiteBwdEmpty);
+      if (*abort) return;  // no further copies: see the drain
+      mbar_arrive_expect_tx(&bars.full[f.slot], TB);
+      load_tile<D>(slots + f.slot * TB, KEY ? (which ? &p.tm_q : &p.tm_do) : (which ? &p.tm_v : &p.tm_k),
+                   &bars.full[f.slot], h, t * kTile, u.b, policy);
+      copies.note(16 * KEY + f.slot, f.fill);
+    }
+    if constexpr (KEY) {
+      if (first + i == 0) {  // the statistics come from the kernel before this one
+        griddep_wait();
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+      }
+      const int x = first + i, s = x & 1;
+      if (x >= 2) mbar_wait(&bars.stat_empty[s], (x / 2 + 1) & 1, abort, p.status, kSiteBwdStat);
+      if (*abort) return;
+      mbar_arrive_expect_tx(&bars.stat_full[s], kStatBytes);
+      bulk_load(smem + C::kOffStat + s * kStatBytes, p.stat + (((int64_t)u.b * p.Hq + h) * p.T + t) * 256, kStatBytes,
+                &bars.stat_full[s]);
+      copies.note(16 + C::kSlots + s, x >> 1);
+    }
+    if (i == 0) {
+      if (r > 0 && same) mbar_wait(&ctl.acc, (r - 1) & 1, abort, p.status, kSiteBwdAcc);
+      if (*abort) return;
+      mbar_arrive_expect_tx(&ctl.resident, 2 * TB);
+      copies.note(Copies::kResident, r);
+      load_tile<D>(smem, KEY ? &p.tm_k : &p.tm_q, &ctl.resident, u.h, u.tile * kTile, u.b, policy);
+      load_tile<D>(smem + TB, KEY ? &p.tm_v : &p.tm_do, &ctl.resident, u.h, u.tile * kTile, u.b, policy);
+    }
+    if (++t == u.first + u.per) {
+      t = u.first;
+      ++h;
+    }
+  }
+}
+
+// After an abort nothing may have waited for the last copies: wait for them (bounded) before the CTA
+// gives up its shared memory.
+template <int D>
+__device__ __forceinline__ void drain_copies(const BwdParams& p, Ctl<D>& ctl, const Copies& copies) {
+  constexpr int NS = BwdCfg<D>::kSlots;
+  static_assert(NS + 2 <= Copies::kResident, "bits of Copies");
+  int no_abort = 0;
+  for (int bit = 0; bit < 32; ++bit) {
+    if (!(copies.issued & (1u << bit))) continue;
+    StepBars<D>& bars = ctl.kind[bit >> 4];
+    const int s = bit & 15;
+    uint64_t* bar = bit == Copies::kResident ? &ctl.resident
+                    : bit == Copies::kResponse || bit == Copies::kResponse + 1 ? &ctl.resp_full[bit - Copies::kResponse]
+                    : s < NS ? &bars.full[s] : &bars.stat_full[s - NS];
+    mbar_wait(bar, (copies.parity >> bit) & 1, &no_abort, p.status, kSiteBwdDrain);
+  }
+}
+
+// MMA issuers: two warps, one per chain of dependences. Chain 0 (warp 1) issues the scores and the
+// products of P (key unit) or of dS (query unit); chain 1 (warp 2) issues dP and, in a key unit, the
+// products of dS. A whole warp runs each loop, so that slots and descriptors are computed in uniform
+// registers, and one elected lane issues each product: issued from a loop that only one lane runs,
+// every tcgen05.mma took about 100 cycles to issue (64 to execute) and the loop was bound by that;
+// with one such warp for both chains its waits and commits still left the tensor core idle.
+template <int D, bool KEY, int CHAIN>
+__device__ __forceinline__ void issue_mmas(const BwdParams& p, int n, uint8_t* smem, Ctl<D>& ctl, int r, int first,
+                                           bool same) {
+  using C = BwdCfg<D>;
+  using L = Layout<D, KEY>;
+  constexpr int TB = C::kTileBytes;
+  // At d = 128, where the tensor core is the bound, a turn keeps its order: what the math warps need
+  // next goes first (key unit: the next scores before dK's product; query unit: the next dP before
+  // dQ's). Key step 2581 against 2756 cycles. At d = 64 the math warps are the bound, and waiting
+  // for the turn costs more than the order gains (key step 2208 against 1988 cycles).
+  constexpr bool kTurns = D == 128;
+  StepBars<D>& bars = ctl.kind[KEY];
+  volatile int* abort = &ctl.abort;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem, 0);
   const uint64_t a = make_sdesc_sw128(smem_u32(smem) + CHAIN * TB, 16, 1024);         // this chain's resident tile
   const uint64_t bk = make_sdesc_sw128(smem_u32(smem + 2 * TB), 16, 1024);            // K-major view of slot 0
   const uint64_t bm = make_sdesc_sw128(smem_u32(smem + 2 * TB), C::kSubBytes, 1024);  // MN-major view of slot 0
-  auto wait_full = [&](int it) { mbar_wait(&ctl.full[it % NS], (it / NS) & 1, abort, p.status, kSiteBwdFull); };
-  auto slot = [&](int it) { return (uint64_t)((it % NS) * (TB >> 4)); };
-  // streamed items: key unit dO_i = 2 i, Q_i = 2 i + 1; query unit K_j = 2 j, V_j = 2 j + 1
-  constexpr int kScoreItem = KEY ? 1 : 0;  // S^T = K Q_i^T, S = Q K_j^T
-  constexpr int kProbItem = KEY ? 0 : 1;   // dP^T = V dO_i^T, dP = dO V_j^T
-  auto scores = [&](int i) {
-    const int it = 2 * i + kScoreItem;
-    wait_full(it);
+  auto wait_full = [&](int x, int which) {
+    const auto f = L::slot_of(x, which);
+    mbar_wait(&bars.full[f.slot], f.fill & 1, abort, p.status, kSiteBwdFull);
+  };
+  auto wait_ds = [&](int x) { mbar_wait(&bars.ds, x & 1, abort, p.status, kSiteBwdDs); };
+  auto wait_turn = [&](int x) {
+    if (kTurns) mbar_wait(&bars.turn[x & 1], (x >> 1) & 1, abort, p.status, kSiteBwdTurn);
+  };
+  auto give_turn = [&](int x) {
+    if (kTurns && elect_one()) mbar_arrive(&bars.turn[x & 1]);
+    __syncwarp();
+  };
+  // the accumulators of the CTA's previous unit have been read
+  auto wait_acc_free = [&]() {
+    if (r > 0) mbar_wait(&ctl.acc_free, (r - 1) & 1, abort, p.status, kSiteBwdAccFree);
+  };
+  // A slot is released by the products that read it: in a key unit one of each chain.
+  // scores: S^T = K Q_i^T, S = Q K_j^T; dprob: dP^T = V dO_i^T, dP = dO V_j^T
+  auto tile_product = [&](int x, int which, uint32_t col, uint64_t* ready, bool release) {
+    const int slot = L::slot_of(x, which).slot;
+    wait_full(x, which);
     __syncwarp();
     tc_fence_after();
     if (elect_one()) {
-      mma_scores<D>(tmem + L::col_s(i), a, bk + slot(it));
-      mma_commit(&ctl.s[L::s_bar(i)]);
-      if (KEY) mma_commit(&ctl.empty[it % NS]);  // with the other chain's arrival, Q_i is released
+      mma_scores<D>(tmem + col, a, bk + (uint64_t)(slot * (TB >> 4)));
+      mma_commit(ready);
+      if (release) mma_commit(&bars.empty[slot]);
     }
     __syncwarp();
   };
-  auto dprob = [&](int i) {
-    const int it = 2 * i + kProbItem;
-    wait_full(it);
+  auto scores = [&](int x) { tile_product(x, KEY ? 1 : 0, L::col_s(x), &bars.s[L::s_bar(x)], KEY); };
+  auto dprob = [&](int x) { tile_product(x, KEY ? 0 : 1, L::kColDp, &bars.dp, true); };
+  // the product of P or dS (TMEM columns a_col) with a streamed tile
+  auto accumulate = [&](uint32_t acc, uint32_t a_col, int x, int which, bool add) {
+    const int slot = L::slot_of(x, which).slot;
     __syncwarp();
     tc_fence_after();
     if (elect_one()) {
-      mma_scores<D>(tmem + L::kColDp, a, bk + slot(it));
-      mma_commit(&ctl.dp);
-      mma_commit(&ctl.empty[it % NS]);
+      mma_accumulate<D>(tmem + acc, tmem + a_col, bm + (uint64_t)(slot * (TB >> 4)), add);
+      mma_commit(&bars.empty[slot]);
     }
     __syncwarp();
   };
-  mbar_wait(&ctl.resident, 0, abort, p.status, kSiteBwdResident);
+  mbar_wait(&ctl.resident, r & 1, abort, p.status, kSiteBwdResident);
+  if (!same) wait_acc_free();  // the kinds place their accumulators and scores differently
   if constexpr (CHAIN == 0) {
-    scores(0);
-    if (L::kBufs == 2 && n > 1) scores(1);
-    for (int i = 0; i < n; ++i) {
-      const int it = 2 * i;  // dO_i, or K_j
-      if (KEY) {
-        wait_full(it);
-        mbar_wait(&ctl.p[i & 1], (i >> 1) & 1, abort, p.status, kSiteBwdP);
-      } else {
-        mbar_wait(&ctl.ds, i & 1, abort, p.status, kSiteBwdDs);
-      }
-      __syncwarp();
-      tc_fence_after();
-      if (elect_one()) {
-        mma_accumulate<D>(tmem, tmem + L::col_s(i), bm + slot(it), i > 0);  // dV += P^T dO_i, dQ += dS K_j
-        mma_commit(&ctl.empty[it % NS]);
-      }
-      __syncwarp();
-      if (i + L::kBufs < n) scores(i + L::kBufs);  // into the buffer that P_i, or dS_j, leaves
-    }
+    scores(first);
+    if (L::kBufs == 2 && n > 1) scores(first + 1);
   } else {
-    dprob(0);
-    for (int i = 0; i < n; ++i) {
-      if (!KEY && i + 1 == n) break;
-      mbar_wait(&ctl.ds, i & 1, abort, p.status, kSiteBwdDs);  // dS_i is written, and dP_i has been read
-      if (KEY) {
-        const int it = 2 * i + 1;
-        wait_full(it);
-        __syncwarp();
-        tc_fence_after();
-        if (elect_one()) {
-          mma_accumulate<D>(tmem + D, tmem + L::kColDp, bm + slot(it), i > 0);  // dK += dS^T Q_i
-          mma_commit(&ctl.empty[it % NS]);
-        }
-        __syncwarp();
-      }
-      if (i + 1 < n) dprob(i + 1);
+    dprob(first);
+  }
+  for (int i = 0; i < n; ++i) {
+    const int x = first + i;
+    if constexpr (KEY && CHAIN == 0) {
+      wait_full(x, 0);
+      mbar_wait(&bars.p[x & 1], (x >> 1) & 1, abort, p.status, kSiteBwdP);
+      if (i == 0) wait_acc_free();
+      accumulate(0, L::col_s(x), x, 0, i > 0);     // dV += P^T dO_i
+      if (i + L::kBufs < n) scores(x + L::kBufs);  // into the buffer P_i leaves
+      give_turn(x);
+    } else if constexpr (KEY) {
+      wait_ds(x);
+      wait_full(x, 1);
+      wait_turn(x);
+      if (i == 0) wait_acc_free();
+      accumulate(D, L::kColDp, x, 1, i > 0);       // dK += dS^T Q_i
+      if (i + 1 < n) dprob(x + 1);
+    } else if constexpr (CHAIN == 0) {
+      wait_ds(x);
+      wait_turn(x);
+      if (i == 0) wait_acc_free();
+      accumulate(0, L::col_s(x), x, 0, i > 0);     // dQ += dS K_j
+      if (i + 2 < n) scores(x + 2);                // into the buffer dS_j leaves
+    } else {
+      wait_ds(x);                                  // dP_j has been read
+      if (i + 1 < n) dprob(x + 1);
+      give_turn(x);
     }
   }
-  // every MMA has completed before TMEM is released (the barrier counts both chains)
   __syncwarp();
-  if (elect_one()) mma_commit(&ctl.acc);
+  if (elect_one()) mma_commit(&ctl.acc);  // the barrier counts both chains
   __syncwarp();
-  int no_abort = 0;
-  mbar_wait(&ctl.acc, 0, &no_abort, p.status, kSiteBwdDrain);
+}
+
+// Overwrite this row's TMEM columns outside [lo, hi) of the 64 at taddr.
+__device__ __forceinline__ void mask_columns(uint32_t taddr, int lo, int hi, uint32_t value) {
+#pragma unroll 1
+  for (int cc = 0; cc < 2; ++cc) {
+    uint32_t r[32];
+    tmem_ld32(taddr + 32 * cc, r);
+    tmem_ld_wait(r);
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if (32 * cc + c < lo || 32 * cc + c >= hi) r[c] = value;
+    tmem_st32(taddr + 32 * cc, r);
+  }
+  tmem_st_wait();
 }
 
 // P and dS of one row's 64 columns per step, then the gradients' epilogue.
 template <int D, bool KEY>
-__device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u, uint8_t* smem, Ctl<D>& ctl,
-                                           uint32_t tmem) {
+__device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u, uint8_t* smem, Ctl<D>& ctl, int r,
+                                           int first) {
   using C = BwdCfg<D>;
   using L = Layout<D, KEY>;
+  StepBars<D>& bars = ctl.kind[KEY];
   volatile int* abort = &ctl.abort;
+  const uint32_t tmem = ctl.tmem;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = (warp - 4) >> 2;
   const int row = (warp & 3) * 32 + lane;
@@ -348,7 +468,7 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
     ndelta2 = f32x2(st[128 + row], st[128 + row]);
   }
   int t = u.first;
-  for (int i = 0; i < u.steps; ++i) {
+  for (int i = first; i < first + u.steps; ++i) {  // counted over the CTA's units of this kind
     // columns [lo, hi) of this row's 64 are not masked
     int lo = 0, hi = 64;
     if (p.causal && t == u.tile) {
@@ -360,12 +480,15 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
     // key unit: the statistics of the columns (every lane reads the same 16 bytes)
     const ulonglong2* st =
         reinterpret_cast<const ulonglong2*>(smem + C::kOffStat + (i & 1) * kStatBytes + 64 * g * sizeof(float));
-    if (KEY) mbar_wait(&ctl.stat_full[i & 1], (i >> 1) & 1, abort, p.status, kSiteBwdStat);
-    mbar_wait(&ctl.s[L::s_bar(i)], L::s_parity(i), abort, p.status, kSiteBwdS);
+    if (KEY) mbar_wait(&bars.stat_full[i & 1], (i >> 1) & 1, abort, p.status, kSiteBwdStat);
+    mbar_wait(&bars.s[L::s_bar(i)], L::s_parity(i), abort, p.status, kSiteBwdS);
     __syncwarp();
     tc_fence_after();
     uint64_t pr[32];  // P of this row's 64 columns, in pairs
     const uint32_t ts = tmem + L::col_s(i) + half_off;
+    // Masked tiles (few): the masked scores become -inf in TMEM, and dP there 0 below, so that the
+    // path every tile takes has no mask in it. (Not 0 times dP: it may be infinite or NaN there.)
+    if (masked) mask_columns(ts, lo, hi, 0xff800000u);
     {
       uint32_t sr[64];
       tmem_ld32(ts, sr);
@@ -384,16 +507,6 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
         pr[2 * k + 1] = f32x2(ex2(x2), ex2(x3));
       }
     }
-    if (masked) {
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        float a, b;
-        split_f32x2(pr[k], a, b);
-        if (2 * k < lo || 2 * k >= hi) a = 0.f;
-        if (2 * k + 1 < lo || 2 * k + 1 >= hi) b = 0.f;
-        pr[k] = f32x2(a, b);
-      }
-    }
     if constexpr (KEY) {  // P^T is dV's A operand, written over this half's scores
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) {
@@ -409,13 +522,14 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.p[i & 1]);
+      if (lane == 0) mbar_arrive(&bars.p[i & 1]);
     }
-    mbar_wait(&ctl.dp, i & 1, abort, p.status, kSiteBwdDp);
+    mbar_wait(&bars.dp, i & 1, abort, p.status, kSiteBwdDp);
     __syncwarp();
     tc_fence_after();
     const uint32_t td = tmem + L::kColDp + half_off;
     const uint32_t t_out = KEY ? td : ts;  // dS goes over dP (key unit) or over the scores
+    if (masked) mask_columns(td, lo, hi, 0u);
     {
       uint32_t dr[64];
       tmem_ld32(td, dr);
@@ -440,14 +554,6 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
           split_f32x2(v1, a, b);
           pk[2 * k + 1] = pack_bf16x2(a, b);
         }
-        if (masked) {  // not 0 times dP: dP may be infinite or NaN where masked
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int c = 32 * cc + 2 * k;
-            if (c < lo || c >= hi) pk[k] &= 0xffff0000u;
-            if (c + 1 < lo || c + 1 >= hi) pk[k] &= 0x0000ffffu;
-          }
-        }
         tmem_st16(t_out + 16 * cc, pk);
       }
     }
@@ -455,16 +561,17 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
     tc_fence_before();
     __syncwarp();
     if (lane == 0) {
-      mbar_arrive(&ctl.ds);
-      if (KEY) mbar_arrive(&ctl.stat_empty[i & 1]);
+      mbar_arrive(&bars.ds);
+      if (KEY) mbar_arrive(&bars.stat_empty[i & 1]);
     }
     if (++t == u.first + u.per) t = u.first;
   }
   // ------------------------------------------------------------ epilogue
-  mbar_wait(&ctl.acc, 0, abort, p.status, kSiteBwdAcc);
+  mbar_wait(&ctl.acc, r & 1, abort, p.status, kSiteBwdAcc);
   __syncwarp();
   tc_fence_after();
-  // key unit: warpgroup 0 stores dV, warpgroup 1 dK; query unit: half of dQ's columns each
+  // Key unit: warpgroup 0 stores dV, warpgroup 1 dK; query unit: half of dQ's columns each. All of the
+  // thread's columns are read before anything is stored, so that the next unit's products may start.
   constexpr int kCols = KEY ? D : D / 2;
   const uint32_t tacc = tmem + lane_off + g * kCols;
   const int heads = KEY ? p.Hkv : p.Hq;
@@ -472,23 +579,53 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
   __nv_bfloat16* base = KEY ? (g == 0 ? p.dv : p.dk) : p.dq + g * kCols;
   base += (((int64_t)u.b * p.S + srow) * heads + u.h) * D;
   const float mul = (KEY && g == 0) ? 1.f : p.scale;
-#pragma unroll 1
+  uint32_t w[kCols / 2];
+#pragma unroll
   for (int cc = 0; cc < kCols / 32; ++cc) {
-    uint32_t r[32];
-    tmem_ld32(tacc + 32 * cc, r);
-    tmem_ld_wait(r);
-    if (srow < p.S) {
-      uint4* dst = reinterpret_cast<uint4*>(base + 32 * cc);
+    uint32_t v[32];
+    tmem_ld32(tacc + 32 * cc, v);
+    tmem_ld_wait(v);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t w[4];
+    for (int k = 0; k < 16; ++k)
+      w[16 * cc + k] = pack_bf16x2(__uint_as_float(v[2 * k]) * mul, __uint_as_float(v[2 * k + 1]) * mul);
+  }
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&ctl.acc_free);
+  if (srow < p.S) {
+    if ((reinterpret_cast<uintptr_t>(base) & 31) == 0) {  // whole 32-byte sectors
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          w[x] = pack_bf16x2(__uint_as_float(r[8 * k + 2 * x]) * mul, __uint_as_float(r[8 * k + 2 * x + 1]) * mul);
-        dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+      for (int k = 0; k < kCols / 16; ++k) st_global_32(base + 16 * k, w + 8 * k);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kCols / 8; ++k)
+        *reinterpret_cast<uint4*>(base + 8 * k) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
     }
   }
+}
+
+// Every product has completed (before TMEM is released; after an abort nobody else waits for them).
+template <int D>
+__device__ __forceinline__ void wait_products(const BwdParams& p, Ctl<D>& ctl, int units) {
+  int no_abort = 0;
+  mbar_wait(&ctl.acc, (units - 1) & 1, &no_abort, p.status, kSiteBwdDrain);
+}
+
+// A warp's walk over the CTA's units: f(unit, units before it, steps before it in units of its kind,
+// whether the unit before it was of its kind). Ends early after an abort; returns the units run.
+template <int D, class F>
+__device__ __forceinline__ int walk_units(const BwdParams& p, Ctl<D>& ctl, F f) {
+  int key_steps = 0, query_steps = 0, last = -1, r = 0;
+  for (int index = blockIdx.x; index >= 0; ++r) {
+    const BwdUnit u = bwd_unit(p, index);
+    f(u, r, u.key ? key_steps : query_steps, last == (int)u.key);
+    __syncwarp();
+    if (u.key) key_steps += u.steps;
+    else query_steps += u.steps;
+    last = u.key;
+    index = taken_unit<D>(p, ctl, r);
+  }
+  return r;
 }
 
 template <int D>
@@ -496,30 +633,38 @@ __global__ void __launch_bounds__(kBwdThreads, 1) bwd_kernel(const __grid_consta
   using C = BwdCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   Ctl<D>& ctl = *reinterpret_cast<Ctl<D>*>(smem + C::kOffCtl);
-  static_assert(sizeof(Ctl<D>) <= 512, "control block too large");
+  static_assert(sizeof(Ctl<D>) <= C::kCtlBytes, "control block too large");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (smem_u32(smem) & 1023u) {  // the swizzled tiles need 1024-byte alignment
     if (threadIdx.x == 0 && atomicCAS(&p.status->code, 0u, 7u) == 0u) p.status->where = kSiteBwdSmem;
     return;
   }
-  const BwdUnit u = bwd_unit(p);
   if (threadIdx.x == 0) {
     ctl.abort = 0;
-    for (int s = 0; s < C::kSlots; ++s) {
-      mbar_init(&ctl.full[s], 1);
-      mbar_init(&ctl.empty[s], u.key ? 2 : 1);  // products that read the tile: both chains, or one
+    for (int kind = 0; kind < 2; ++kind) {
+      StepBars<D>& bars = ctl.kind[kind];
+      for (int s = 0; s < C::kSlots; ++s) {
+        mbar_init(&bars.full[s], 1);
+        mbar_init(&bars.empty[s], kind ? 2 : 1);  // products that read a slot
+      }
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(&bars.s[s], 1);
+        mbar_init(&bars.p[s], 8);  // two: a warp may reach step i + 1 before another has finished step i
+        mbar_init(&bars.turn[s], 1);
+        mbar_init(&bars.stat_full[s], 1);
+        mbar_init(&bars.stat_empty[s], 8);  // one arrival per math warp
+      }
+      mbar_init(&bars.dp, 1);
+      mbar_init(&bars.ds, 8);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&ctl.s[s], 1);
-      mbar_init(&ctl.p[s], 8);  // two: a warp may reach step i + 1 before another has finished step i
-      mbar_init(&ctl.stat_full[s], 1);
-      mbar_init(&ctl.stat_empty[s], 8);  // one arrival per math warp
+      mbar_init(&ctl.resp_full[s], 1);
+      mbar_init(&ctl.resp_empty[s], kBwdWalkers);
     }
     mbar_init(&ctl.resident, 1);
-    mbar_init(&ctl.dp, 1);
-    mbar_init(&ctl.ds, 8);
     mbar_init(&ctl.acc, 2);
+    mbar_init(&ctl.acc_free, 8);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -529,31 +674,54 @@ __global__ void __launch_bounds__(kBwdThreads, 1) bwd_kernel(const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl.tmem;
 
-  if (warp >= 4) {
-    regs_inc<kRegsBwdMath>();
-    if (u.key) math_warps<D, true>(p, u, smem, ctl, tmem);
-    else math_warps<D, false>(p, u, smem, ctl, tmem);
-  } else {
+  // (each register budget is set inside the branch of its role, where the compiler sees it)
+  if (warp == 0) {
     regs_dec<kRegsBwdControl>();
-    if (warp == 0 && lane == 0) {
-      if (u.key) produce<D, true>(p, u, smem, ctl);
-      else produce<D, false>(p, u, smem, ctl);
-    } else if (warp == 1) {
-      if (u.key) issue_mmas<D, true, 0>(p, u.steps, smem, ctl, tmem);
-      else issue_mmas<D, false, 0>(p, u.steps, smem, ctl, tmem);
-    } else if (warp == 2) {
-      if (u.key) issue_mmas<D, true, 1>(p, u.steps, smem, ctl, tmem);
-      else issue_mmas<D, false, 1>(p, u.steps, smem, ctl, tmem);
-    }
-    __syncwarp();
+    Copies copies;
+    walk_units<D>(p, ctl, [&](const BwdUnit& u, int r, int first, bool same) {
+      if (lane != 0) return;
+      volatile int* abort = &ctl.abort;
+      if (u.key) produce<D, true>(p, u, smem, ctl, r, first, same, copies);
+      else produce<D, false>(p, u, smem, ctl, r, first, same, copies);
+      // ask for the next unit (the slot's previous response must have been read)
+      if (r >= 2) mbar_wait(&ctl.resp_empty[r & 1], ((r >> 1) + 1) & 1, abort, p.status, kSiteBwdTake);
+      if (!*abort) {
+        fence_proxy_async_smem();
+        mbar_arrive_expect_tx(&ctl.resp_full[r & 1], 16);
+        launch_cancel_request(&ctl.resp[r & 1], &ctl.resp_full[r & 1]);
+        copies.note(Copies::kResponse + (r & 1), r >> 1);
+      }
+    });
+    if (lane == 0 && ctl.abort) drain_copies<D>(p, ctl, copies);
+  } else if (warp == 1) {
+    regs_dec<kRegsBwdControl>();
+    const int units = walk_units<D>(p, ctl, [&](const BwdUnit& u, int r, int first, bool same) {
+      if (u.key) issue_mmas<D, true, 0>(p, u.steps, smem, ctl, r, first, same);
+      else issue_mmas<D, false, 0>(p, u.steps, smem, ctl, r, first, same);
+    });
+    wait_products<D>(p, ctl, units);
+  } else if (warp == 2) {
+    regs_dec<kRegsBwdControl>();
+    const int units = walk_units<D>(p, ctl, [&](const BwdUnit& u, int r, int first, bool same) {
+      if (u.key) issue_mmas<D, true, 1>(p, u.steps, smem, ctl, r, first, same);
+      else issue_mmas<D, false, 1>(p, u.steps, smem, ctl, r, first, same);
+    });
+    wait_products<D>(p, ctl, units);
+  } else if (warp == 3) {
+    regs_dec<kRegsBwdControl>();
+  } else {
+    regs_inc<kRegsBwdMath>();
+    walk_units<D>(p, ctl, [&](const BwdUnit& u, int r, int first, bool) {
+      if (u.key) math_warps<D, true>(p, u, smem, ctl, r, first);
+      else math_warps<D, false>(p, u, smem, ctl, r, first);
+    });
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(ctl.tmem, 512);
   }
 }
 
