@@ -430,6 +430,24 @@ __device__ __forceinline__ void issue_mmas(const BwdParams& p, int n, uint8_t* s
   __syncwarp();
 }
 
+// TMEM accesses of 16 lanes in matrix-fragment form: thread 4 a + b of the warp holds, of lanes a and
+// a + 8, the 64-bit (load: columns 8 q + 2 b, + 1) or 32-bit (store: column 4 q + b) words of each
+// group q. Load: r[4 q], r[4 q + 1] of lane a, r[4 q + 2], r[4 q + 3] of lane a + 8; store: r[2 q] of
+// lane a, r[2 q + 1] of lane a + 8.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
+}
+
 // Overwrite this row's TMEM columns outside [lo, hi) of the 64 at taddr.
 __device__ __forceinline__ void mask_columns(uint32_t taddr, int lo, int hi, uint32_t value) {
 #pragma unroll 1
@@ -477,19 +495,49 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
     }
     if (!KEY && (t + 1) * kTile > p.S) hi = min(hi, p.S - t * kTile - 64 * g);
     const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < 64);
-    // key unit: the statistics of the columns (every lane reads the same 16 bytes)
-    const ulonglong2* st =
-        reinterpret_cast<const ulonglong2*>(smem + C::kOffStat + (i & 1) * kStatBytes + 64 * g * sizeof(float));
+    // Key unit: the statistics belong to the columns. In fragment form a thread has 16 of the 64
+    // columns (of four rows); with whole rows per thread, reading all 64 pairs of statistics from
+    // shared memory took 500 cycles of each step.
+    const uint64_t* st = reinterpret_cast<const uint64_t*>(smem + C::kOffStat + (i & 1) * kStatBytes) + 32 * g +
+                         (lane & 3);
     if (KEY) mbar_wait(&bars.stat_full[i & 1], (i >> 1) & 1, abort, p.status, kSiteBwdStat);
     mbar_wait(&bars.s[L::s_bar(i)], L::s_parity(i), abort, p.status, kSiteBwdS);
     __syncwarp();
     tc_fence_after();
-    uint64_t pr[32];  // P of this row's 64 columns, in pairs
+    uint64_t pr[32];  // P: 64 values in pairs
     const uint32_t ts = tmem + L::col_s(i) + half_off;
     // Masked tiles (few): the masked scores become -inf in TMEM, and dP there 0 below, so that the
     // path every tile takes has no mask in it. (Not 0 times dP: it may be infinite or NaN there.)
     if (masked) mask_columns(ts, lo, hi, 0xff800000u);
-    {
+    if constexpr (KEY) {
+      uint32_t sr[64];
+      tmem_ld_frag(ts, sr);
+      tmem_ld_frag(ts + (16u << 16), sr + 32);
+      uint64_t nl[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) nl[q] = st[4 * q];
+      tmem_ld_wait(sr);
+      tmem_ld_wait(sr + 32);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const uint32_t* v = sr + 32 * h + 2 * k;
+          float x0, x1;
+          split_f32x2(fma_f32x2(f32x2(__uint_as_float(v[0]), __uint_as_float(v[1])), c2, nl[k >> 1]), x0, x1);
+          x0 = ex2(x0);
+          x1 = ex2(x1);
+          pr[16 * h + k] = f32x2(x0, x1);
+          pk[k] = pack_bf16x2(x0, x1);
+        }
+        tmem_st_frag(ts + ((16u * h) << 16), pk);  // P^T is dV's A operand, written over the scores
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.p[i & 1]);
+    } else {
       uint32_t sr[64];
       tmem_ld32(ts, sr);
       tmem_ld32(ts + 32, sr + 32);
@@ -497,40 +545,41 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
       tmem_ld_wait(sr + 32);
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        ulonglong2 nl;
-        if constexpr (KEY) nl = st[k];
-        else nl = make_ulonglong2(nlse2, nlse2);
         float x0, x1, x2, x3;
-        split_f32x2(fma_f32x2(f32x2(__uint_as_float(sr[4 * k]), __uint_as_float(sr[4 * k + 1])), c2, nl.x), x0, x1);
-        split_f32x2(fma_f32x2(f32x2(__uint_as_float(sr[4 * k + 2]), __uint_as_float(sr[4 * k + 3])), c2, nl.y), x2, x3);
+        split_f32x2(fma_f32x2(f32x2(__uint_as_float(sr[4 * k]), __uint_as_float(sr[4 * k + 1])), c2, nlse2), x0, x1);
+        split_f32x2(fma_f32x2(f32x2(__uint_as_float(sr[4 * k + 2]), __uint_as_float(sr[4 * k + 3])), c2, nlse2), x2, x3);
         pr[2 * k] = f32x2(ex2(x0), ex2(x1));
         pr[2 * k + 1] = f32x2(ex2(x2), ex2(x3));
       }
-    }
-    if constexpr (KEY) {  // P^T is dV's A operand, written over this half's scores
-#pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          float a, b;
-          split_f32x2(pr[16 * cc + k], a, b);
-          pk[k] = pack_bf16x2(a, b);
-        }
-        tmem_st16(ts + 16 * cc, pk);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.p[i & 1]);
     }
     mbar_wait(&bars.dp, i & 1, abort, p.status, kSiteBwdDp);
     __syncwarp();
     tc_fence_after();
     const uint32_t td = tmem + L::kColDp + half_off;
-    const uint32_t t_out = KEY ? td : ts;  // dS goes over dP (key unit) or over the scores
     if (masked) mask_columns(td, lo, hi, 0u);
-    {
+    if constexpr (KEY) {
+      uint32_t dr[64];
+      tmem_ld_frag(td, dr);
+      tmem_ld_frag(td + (16u << 16), dr + 32);
+      uint64_t nd[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) nd[q] = st[64 + 4 * q];
+      tmem_ld_wait(dr);
+      tmem_ld_wait(dr + 32);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const uint32_t* v = dr + 32 * h + 2 * k;
+          float a, b;
+          split_f32x2(mul_f32x2(pr[16 * h + k], add_f32x2(f32x2(__uint_as_float(v[0]), __uint_as_float(v[1])),
+                                                          nd[k >> 1])), a, b);
+          pk[k] = pack_bf16x2(a, b);
+        }
+        tmem_st_frag(td + ((16u * h) << 16), pk);  // dS^T over dP^T
+      }
+    } else {
       uint32_t dr[64];
       tmem_ld32(td, dr);
       tmem_ld32(td + 32, dr + 32);
@@ -539,22 +588,14 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
         uint32_t pk[16];
         tmem_ld_wait(dr + 32 * cc);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          ulonglong2 nd;
-          if constexpr (KEY) nd = st[32 + 8 * cc + k];
-          else nd = make_ulonglong2(ndelta2, ndelta2);
-          const uint32_t* d4 = dr + 32 * cc + 4 * k;
-          const uint64_t v0 = mul_f32x2(pr[16 * cc + 2 * k],
-                                        add_f32x2(f32x2(__uint_as_float(d4[0]), __uint_as_float(d4[1])), nd.x));
-          const uint64_t v1 = mul_f32x2(pr[16 * cc + 2 * k + 1],
-                                        add_f32x2(f32x2(__uint_as_float(d4[2]), __uint_as_float(d4[3])), nd.y));
+        for (int k = 0; k < 16; ++k) {
+          const uint32_t* v = dr + 32 * cc + 2 * k;
           float a, b;
-          split_f32x2(v0, a, b);
-          pk[2 * k] = pack_bf16x2(a, b);
-          split_f32x2(v1, a, b);
-          pk[2 * k + 1] = pack_bf16x2(a, b);
+          split_f32x2(mul_f32x2(pr[16 * cc + k], add_f32x2(f32x2(__uint_as_float(v[0]), __uint_as_float(v[1])),
+                                                           ndelta2)), a, b);
+          pk[k] = pack_bf16x2(a, b);
         }
-        tmem_st16(t_out + 16 * cc, pk);
+        tmem_st16(ts + 16 * cc, pk);  // dS over the scores
       }
     }
     tmem_st_wait();
