@@ -231,6 +231,66 @@ fa_status fa_paged_append(const void* k_new, const void* v_new, const int32_t* c
                           int Hkv, int d, void* k_pages, void* v_pages, fa_stream_t stream);
 
 /*
+ * RMS norm of each query and key head and the rotary position embedding, in one pass over q and k:
+ * what a model applies between its projections and fa_fwd, or fa_paged_append and fa_paged_fwd
+ * (T is then B * S, or the new tokens of a batch, down to one). The pages define neither.
+ *   q, q_out: [T, Hq, d] bf16;  k, k_out: [T, Hkv, d] bf16. The heads of a token are contiguous;
+ *   tokens are `*_stride` elements apart (a multiple of 8, at least heads * d), so that a tensor may
+ *   be a view of a fused projection.
+ *   q_weight, k_weight: [d] bf16, or both NULL: no norm (eps is then ignored).
+ *   positions: [num_axes, T] int32, any values;  inv_freq: [rot_dim / 2] fp32 (a scaled or truncated
+ *   set of frequencies is the caller's to make).
+ *   rot_dim: rotated elements of each head, a multiple of 16, at most d; 0: norm only (positions and
+ *   inv_freq are then ignored, and weights are required).
+ *   sections: num_axes (1 to 4) counts on the HOST that add up to rot_dim / 2: the first sections[0]
+ *   pairs turn with positions[0], the next sections[1] with positions[1] and so on (time, height and
+ *   width of image and video tokens, for instance). NULL with one axis.
+ *   interleaved: 0: pair i is elements (i, i + rot_dim / 2); 1: elements (2i, 2i + 1).
+ * For each head x: z = x * q_weight / sqrt(mean(x^2) + eps) (z = x without weights), and for each pair
+ * (a, b) of z with phi = positions[axis][t] * inv_freq[i]:
+ *     a' = a cos(phi) - b sin(phi);   b' = b cos(phi) + a sin(phi)
+ * phi is reduced to one turn exactly (64-bit fixed point) before cos and sin; the norm and the
+ * rotation are fp32, rounded to bf16 once at the end. The sum of squares is fp32 too: it overflows for
+ * |x| beyond about 1e18.
+ * q_out may be q itself (same pointer and stride) and k_out k; no output shares memory with another
+ * tensor of the call otherwise.
+ * Errors: FA_ERR_INVALID_ARG (null pointer, negative T, non-positive heads, a stride below heads * d,
+ * eps not positive, one weight without the other, sections that do not add up, overlapping memory),
+ * FA_ERR_UNSUPPORTED (d not 64 or 128, rot_dim not a multiple of 16, more than 4 axes, too large),
+ * FA_ERR_ALIGNMENT (bf16 tensors 16 bytes, strides 8 elements, others 4 bytes), FA_ERR_CUDA.
+ * T == 0 succeeds and does nothing. Asynchronous on `stream`; allocates nothing.
+ */
+fa_status fa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                          const void* q_weight, const void* k_weight, float eps,
+                          const int32_t* positions, const float* inv_freq, int num_axes,
+                          const int32_t* sections, int rot_dim, int interleaved, int64_t T, int Hq,
+                          int Hkv, int d, void* q_out, int64_t q_out_stride, void* k_out,
+                          int64_t k_out_stride, fa_stream_t stream);
+
+/*
+ * Backward of fa_qk_norm_rope (same meaning of the shared arguments).
+ *   dq_out, dk_out: gradients with respect to q_out and k_out;  dq, dk: with respect to q and k
+ *   (bf16, each with its own token stride; dq may be dq_out or q itself, dk likewise);
+ *   q, k: the forward pass's inputs, before the norm (ignored without weights);
+ *   dq_weight, dk_weight: [d] fp32, written (ignored without weights): sums over all tokens and heads,
+ *   in fp32 and in a fixed order: the same inputs give the same bits. T == 0 gives zeros.
+ *   workspace: fa_qk_norm_rope_bwd_workspace_bytes(...) bytes, 256-byte aligned (without weights it may
+ *   be NULL); calls that share one must be ordered on one stream.
+ * Errors as for fa_qk_norm_rope; FA_ERR_WORKSPACE.
+ */
+fa_status fa_qk_norm_rope_bwd(const void* dq_out, int64_t dq_out_stride, const void* dk_out,
+                              int64_t dk_out_stride, const void* q, int64_t q_stride, const void* k,
+                              int64_t k_stride, const void* q_weight, const void* k_weight, float eps,
+                              const int32_t* positions, const float* inv_freq, int num_axes,
+                              const int32_t* sections, int rot_dim, int interleaved, int64_t T, int Hq,
+                              int Hkv, int d, void* dq, int64_t dq_stride, void* dk, int64_t dk_stride,
+                              float* dq_weight, float* dk_weight, void* workspace,
+                              size_t workspace_bytes, fa_stream_t stream);
+
+/* Workspace bytes fa_qk_norm_rope_bwd needs with weights (partial sums of their gradients). */
+size_t fa_qk_norm_rope_bwd_workspace_bytes(int64_t T, int Hq, int Hkv, int d);
+
+/*
  * Split-KV paged decode for callers that cannot allocate device memory. The pages have no
  * counterpart of this entry point; it exists for callers that may not call cudaMalloc (for
  * example an engine whose device memory is all handed to a fixed arena, or a plugin inside a

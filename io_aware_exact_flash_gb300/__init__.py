@@ -1,5 +1,5 @@
-"""Exact attention forward for GB300 (sm_103a): dense, paged/ragged prefill, split-KV decode and
-the paged KV append that feeds them.
+"""Exact attention for GB300 (sm_103a): dense forward and backward, paged/ragged prefill, split-KV
+decode, the paged KV append that feeds them, and the query/key norm with rotary positions before them.
 
 The compute path is the C-ABI library ``libfa_gb300.so`` (declared in ``include/fa.h``); this
 package is its thin binding plus the seeded workload generator used by tests and benchmarks.
@@ -19,6 +19,9 @@ from .binding import (  # noqa: F401
     fa_paged_decode_noalloc,
     fa_paged_fwd,
     fa_paged_num_splits,
+    fa_qk_norm_rope,
+    fa_qk_norm_rope_bwd,
+    fa_qk_norm_rope_bwd_workspace_bytes,
     fa_selftest_wait_timeout,
     fa_paged_workspace_bytes,
     load_library,

@@ -28,7 +28,8 @@ _STATUS_NAMES = {
 EXPORTED = ("fa_status_string", "fa_fwd", "fa_paged_fwd", "fa_paged_workspace_bytes",
             "fa_decode_num_splits", "fa_merge_states", "fa_get_device_status", "fa_paged_decode_noalloc",
             "fa_selftest_wait_timeout", "fa_paged_append", "fa_cascade_fwd", "fa_cascade_workspace_bytes",
-            "fa_paged_num_splits", "fa_bwd", "fa_bwd_workspace_bytes")
+            "fa_paged_num_splits", "fa_bwd", "fa_bwd_workspace_bytes", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd",
+            "fa_qk_norm_rope_bwd_workspace_bytes")
 
 
 class FaError(RuntimeError):
@@ -85,6 +86,14 @@ def load_library(path: str = None) -> ctypes.CDLL:
     lib.fa_bwd_workspace_bytes.restype = sz
     lib.fa_bwd.argtypes = [vp] * 10 + [i] * 6 + [f, vp, sz, vp]
     lib.fa_bwd.restype = i
+    i64 = ctypes.c_int64
+    rope = [vp, vp, f, vp, vp, i, vp, i, i, i64, i, i, i]
+    lib.fa_qk_norm_rope.argtypes = [vp, i64] * 2 + rope + [vp, i64] * 2 + [vp]
+    lib.fa_qk_norm_rope.restype = i
+    lib.fa_qk_norm_rope_bwd.argtypes = [vp, i64] * 4 + rope + [vp, i64] * 2 + [vp, vp, vp, sz, vp]
+    lib.fa_qk_norm_rope_bwd.restype = i
+    lib.fa_qk_norm_rope_bwd_workspace_bytes.argtypes = [i64, i, i, i]
+    lib.fa_qk_norm_rope_bwd_workspace_bytes.restype = sz
     lib.fa_get_device_status.argtypes = [vp, ctypes.POINTER(i), ctypes.POINTER(i)]
     lib.fa_get_device_status.restype = i
     _lib = lib
@@ -170,14 +179,16 @@ def _one_device(like, tensors):
             raise ValueError(f"{name} is on {t.device}, not on {like.device}")
 
 
-@contextlib.contextmanager
 def _on_device(device, stream):
-    """Make `device` current, and `stream` (default: that device's current stream) the stream that
-    allocations of the call belong to; yields the stream's handle."""
-    if stream is not None and stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-    with torch.cuda.device(device), _on(stream):
-        yield _stream(stream)
+    """Context of a call: `device` is current, and allocations belong to `stream` (default: that
+    device's current stream)."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        return torch.cuda.stream(stream)  # makes its device current too
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
 
 
 def _result(name, t, shape, dtype, device):
@@ -228,13 +239,14 @@ def fa_bwd(q, k, v, out, lse, dout, causal=False, scale=None, dlse=None, dq=None
     _one_device(q, (("k", k), ("v", v), ("out", out), ("lse", lse), ("dout", dout), ("dlse", dlse)))
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     lib = load_library()
-    with _on_device(q.device, stream) as handle:
+    with _on_device(q.device, stream):
         dq = _result("dq", dq, q.shape, q.dtype, q.device)
         dk = _result("dk", dk, k.shape, k.dtype, q.device)
         dv = _result("dv", dv, v.shape, v.dtype, q.device)
         workspace, ws_bytes = _scratch(workspace, fa_bwd_workspace_bytes(B, Hq, Hkv, S, d, causal), q.device)
         code = lib.fa_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dlse), _ptr(dq), _ptr(dk),
-                          _ptr(dv), B, Hq, Hkv, S, d, int(bool(causal)), scale, _ptr(workspace), ws_bytes, handle)
+                          _ptr(dv), B, Hq, Hkv, S, d, int(bool(causal)), scale, _ptr(workspace), ws_bytes,
+                          _stream(stream))
     _check("fa_bwd", code)
     return dq, dk, dv
 
@@ -391,6 +403,124 @@ def fa_paged_append(k_new, v_new, cu_seqlens_new, kv_lens_before, page_table, k_
                                           _ptr(page_table), num_seqs, total_new, page_size, max_pages, num_pages,
                                           Hkv, d, _ptr(k_pages), _ptr(v_pages), _stream(stream))
     _check("fa_paged_append", code)
+
+
+def _token_rows(name, t, shape=None, device=None):
+    """A [T, heads, d] bf16 CUDA tensor whose heads are contiguous within a token (a view of a fused
+    projection, for instance); returns its token stride in elements."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA bfloat16 tensor")
+    if t.dim() != 3 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be [T, heads, d]" + (f" = {tuple(shape)}" if shape is not None else ""))
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    T, H, d = t.shape
+    s_t, s_h, s_d = t.stride()
+    if T == 0:
+        return H * d
+    if (d > 1 and s_d != 1) or (H > 1 and s_h != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return s_t if T > 1 else H * d
+
+
+def _rope_arguments(q, k, positions, inv_freq, q_weight, k_weight, sections):
+    """The arguments that fa_qk_norm_rope and its backward share, checked: (positions, inv_freq,
+    num_axes, sections as a host array, rot_dim)."""
+    T, d, device = q.shape[0], q.shape[2], q.device
+    if k.shape[0] != T or k.shape[2] != d:
+        raise ValueError("q and k must be [T, Hq, d] and [T, Hkv, d]")
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight go together")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None and (w.dtype != torch.bfloat16 or w.shape != (d,) or w.device != device
+                              or not w.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous bfloat16 tensor of {d} elements on {device}")
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq go together")
+    if positions is None:
+        if q_weight is None:
+            raise ValueError("nothing to do: neither weights nor positions")
+        return 1, None, 0
+    if (inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or inv_freq.device != device
+            or not inv_freq.is_contiguous()):
+        raise ValueError(f"inv_freq must be a contiguous 1-D float32 tensor on {device}")
+    num_axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if (positions.dtype != torch.int32 or positions.dim() not in (1, 2) or positions.shape[-1] != T
+            or positions.device != device or not positions.is_contiguous()):
+        raise ValueError(f"positions must be a contiguous int32 tensor [T] or [axes, T] on {device}, T = {T}")
+    pairs = inv_freq.shape[0]
+    if sections is None:
+        if num_axes != 1:
+            raise ValueError("sections must give the pairs of each position axis")
+        return num_axes, None, 2 * pairs
+    if len(sections) != num_axes or sum(sections) != pairs:
+        raise ValueError(f"sections must be {num_axes} counts that add up to {pairs}")
+    return num_axes, (ctypes.c_int32 * num_axes)(*sections), 2 * pairs
+
+
+def fa_qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6, sections=None,
+                    interleaved=False, q_out=None, k_out=None, stream=None):
+    """RMS norm of each query and key head and the rotary position embedding, in one pass.
+
+    q: [T, Hq, d]; k: [T, Hkv, d] (bf16, CUDA; the heads of a token contiguous, tokens any multiple of 8
+    elements apart). q_weight, k_weight: [d] bf16, or both None: no norm. positions: [T], or
+    [axes, T] with sections giving the pairs that turn with each axis (int32, CUDA); inv_freq:
+    [pairs] fp32, where 2 * pairs elements of each head are rotated; both None: norm only.
+    interleaved: pairs are (2i, 2i + 1) instead of (i, i + pairs). q_out may be q and k_out k (in
+    place). Returns (q_out, k_out)."""
+    sq, sk = _token_rows("q", q), _token_rows("k", k, device=q.device)
+    num_axes, host_sections, rot_dim = _rope_arguments(q, k, positions, inv_freq, q_weight, k_weight, sections)
+    T, Hq, d = q.shape
+    lib = load_library()
+    with _on_device(q.device, stream):
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=q.device)
+        so, sp = _token_rows("q_out", q_out, q.shape, q.device), _token_rows("k_out", k_out, k.shape, q.device)
+        code = lib.fa_qk_norm_rope(_ptr(q), sq, _ptr(k), sk, _ptr(q_weight), _ptr(k_weight), float(eps),
+                                   _ptr(positions), _ptr(inv_freq), num_axes, host_sections, rot_dim,
+                                   int(bool(interleaved)), T, Hq, k.shape[1], d, _ptr(q_out), so, _ptr(k_out), sp,
+                                   _stream(stream))
+    _check("fa_qk_norm_rope", code)
+    return q_out, k_out
+
+
+def fa_qk_norm_rope_bwd_workspace_bytes(T, Hq, Hkv, d):
+    return int(load_library().fa_qk_norm_rope_bwd_workspace_bytes(T, Hq, Hkv, d))
+
+
+def fa_qk_norm_rope_bwd(dq_out, dk_out, q, k, positions=None, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6,
+                        sections=None, interleaved=False, dq=None, dk=None, dq_weight=None, dk_weight=None,
+                        workspace=None, stream=None):
+    """Gradients of fa_qk_norm_rope: dq_out, dk_out are those of its results, q and k its inputs (not
+    read without weights). Returns (dq, dk, dq_weight, dk_weight): bf16 like q and k, and fp32 [d]
+    (None without weights). dq may be dq_out and dk dk_out (in place)."""
+    sq, sk = _token_rows("q", q), _token_rows("k", k, device=q.device)
+    sg, sh = _token_rows("dq_out", dq_out, q.shape, q.device), _token_rows("dk_out", dk_out, k.shape, q.device)
+    num_axes, host_sections, rot_dim = _rope_arguments(q, k, positions, inv_freq, q_weight, k_weight, sections)
+    T, Hq, d = q.shape
+    lib = load_library()
+    with _on_device(q.device, stream):
+        if dq is None:
+            dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if dk is None:
+            dk = torch.empty(k.shape, dtype=k.dtype, device=q.device)
+        so, sp = _token_rows("dq", dq, q.shape, q.device), _token_rows("dk", dk, k.shape, q.device)
+        ws_bytes = 0
+        if q_weight is not None:
+            dq_weight = _result("dq_weight", dq_weight, (d,), torch.float32, q.device)
+            dk_weight = _result("dk_weight", dk_weight, (d,), torch.float32, q.device)
+            workspace, ws_bytes = _scratch(workspace, fa_qk_norm_rope_bwd_workspace_bytes(T, Hq, k.shape[1], d), q.device)
+        else:
+            dq_weight = dk_weight = workspace = None
+        code = lib.fa_qk_norm_rope_bwd(_ptr(dq_out), sg, _ptr(dk_out), sh, _ptr(q), sq, _ptr(k), sk, _ptr(q_weight),
+                                       _ptr(k_weight), float(eps), _ptr(positions), _ptr(inv_freq), num_axes,
+                                       host_sections, rot_dim, int(bool(interleaved)), T, Hq, k.shape[1], d, _ptr(dq),
+                                       so, _ptr(dk), sp, _ptr(dq_weight), _ptr(dk_weight), _ptr(workspace), ws_bytes,
+                                       _stream(stream))
+    _check("fa_qk_norm_rope_bwd", code)
+    return dq, dk, dq_weight, dk_weight
 
 
 def fa_get_device_status(stream=None):

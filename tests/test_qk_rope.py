@@ -1,0 +1,209 @@
+"""Per-head RMS norm and rotary positions, forward and backward, on the GPU against the definition in
+fp64, and the backward pass against differences of the definition.
+
+Tolerance. A result is rounded to bf16 once: at most u = 2^-8 of its value. Before that, in fp32
+(u32 = 2^-24): the sum of d <= 128 squares and its root err by less than 2^-18 relative, each product by
+u32; cos and sin of an angle reduced to a fraction of a turn in 32 bits err by at most 2^-22 absolute.
+So a rotated element is off by at most u |y| + 2^-16 (|z_a| + |z_b|), and a gradient dx by at most
+u |dx| + 2^-14 of its terms' magnitudes r (|g w| + |xhat| mean|g w xhat|) of its pair or head. A weight's
+gradient sums n = T heads terms in fp32: a lane's chain, then a tree; each term is off by 2^-15 of its
+magnitude and the chain (at most n terms) by n u32 of the sum of magnitudes; with n below 2^11 here,
+2^-12 of the sum of magnitudes bounds both.
+"""
+import pytest
+import torch
+
+U = 2.0 ** -8
+
+
+def make(T, Hq, Hkv, d, rot, axes, norm, fused=False, seed=0, far=False):
+    g = torch.Generator(device="cuda").manual_seed(seed + 7 * T + Hq + d + rot)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    if fused:  # views of one projection, with the values between them
+        qkv = r(T, (Hq + 2 * Hkv) * d).mul_(1.5).bfloat16()
+        q = qkv[:, :Hq * d].unflatten(1, (Hq, d))
+        k = qkv[:, Hq * d:(Hq + Hkv) * d].unflatten(1, (Hkv, d))
+    else:
+        q, k = r(T, Hq, d).mul_(1.5).bfloat16(), r(T, Hkv, d).mul_(1.5).bfloat16()
+    a = dict(positions=None, inv_freq=None, q_weight=None, k_weight=None, eps=1e-5, sections=None)
+    if rot:
+        lim = 2 ** 31 - 1 if far else 4096
+        pos = torch.randint(-lim if far else 0, lim, (axes, T), generator=g, device="cuda", dtype=torch.int64)
+        a["positions"] = (pos.int() if axes > 1 else pos[0].int()).contiguous()
+        a["inv_freq"] = (10000.0 ** -(torch.arange(rot // 2, device="cuda").double() * 2 / rot)).float()
+        if axes > 1:
+            base = rot // 2 // axes
+            a["sections"] = [rot // 2 - base * (axes - 1)] + [base] * (axes - 1)
+    if norm:
+        a["q_weight"], a["k_weight"] = ((1 + 0.3 * r(d)).bfloat16() for _ in range(2))
+    return q, k, a, r(T, Hq, d).bfloat16(), r(T, Hkv, d).bfloat16()
+
+
+def pairs_of(rot, interleaved, device):
+    i = torch.arange(rot // 2, device=device)
+    return (2 * i, 2 * i + 1) if interleaved else (i, i + rot // 2)
+
+
+def cos_sin(a, T, device):
+    if a["positions"] is None:
+        z = torch.zeros(T, 1, 0, dtype=torch.float64, device=device)
+        return z, z
+    pos = a["positions"].double().reshape(-1, T)
+    sections = a["sections"] or [a["inv_freq"].numel()]
+    axis = torch.tensor([x for x, n in enumerate(sections) for _ in range(n)], device=device)
+    phi = (pos[axis].t() * a["inv_freq"].double()).unsqueeze(1)
+    return phi.cos(), phi.sin()
+
+
+def define(x, w, eps, c, s, ia, ib):
+    """The definition in fp64, differentiable: y, and z before the rotation."""
+    z = x
+    if w is not None:
+        z = x * w / torch.sqrt((x * x).mean(-1, keepdim=True) + eps)
+    y = z.clone()
+    y[..., ia] = z[..., ia] * c - z[..., ib] * s
+    y[..., ib] = z[..., ib] * c + z[..., ia] * s
+    return y, z
+
+
+CASES = [
+    # (T, Hq, Hkv, d, rot, axes, norm, interleaved, fused)
+    (1, 32, 8, 128, 128, 1, True, False, False),    # one token
+    (1, 1, 1, 64, 64, 1, True, True, True),
+    (3, 5, 3, 128, 128, 1, True, False, True),      # heads that do not fill a warp step
+    (7, 9, 1, 64, 32, 1, True, False, False),       # partly rotated
+    (7, 9, 2, 64, 16, 1, False, True, True),        # the smallest rotation, no norm
+    (33, 4, 4, 128, 96, 3, True, True, False),      # rotated part not a power of two, three axes
+    (33, 8, 2, 128, 64, 4, True, False, True),      # four axes
+    (50, 6, 2, 64, 64, 2, False, False, False),
+    (5, 3, 2, 128, 0, 1, True, False, True),        # norm only
+    (257, 32, 8, 128, 128, 1, True, False, True),
+    (1000, 8, 2, 64, 64, 3, True, True, True),
+    (1500, 1, 1, 128, 128, 1, True, False, False),  # more tokens than warps of a small grid
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,Hq,Hkv,d,rot,axes,norm,interleaved,fused", CASES)
+def test_forward_and_backward_match_fp64(T, Hq, Hkv, d, rot, axes, norm, interleaved, fused):
+    import io_aware_exact_flash_gb300 as fa
+
+    q, k, a, dyq, dyk = make(T, Hq, Hkv, d, rot, axes, norm, fused)
+    q0, k0 = q.clone(), k.clone()
+    out = fa.fa_qk_norm_rope(q, k, interleaved=interleaved, **a)
+    dq, dk, dwq, dwk = fa.fa_qk_norm_rope_bwd(dyq, dyk, q, k, interleaved=interleaved, **a)
+    assert torch.equal(q, q0) and torch.equal(k, k0)
+    assert (dwq is None) == (not norm) and (dwk is None) == (not norm)
+    c, s = cos_sin(a, T, q.device)
+    ia, ib = pairs_of(rot, interleaved, q.device)
+    for y, x, wname, dy, dx, dw in ((out[0], q, "q_weight", dyq, dq, dwq), (out[1], k, "k_weight", dyk, dk, dwk)):
+        xd = x.double().requires_grad_(True)
+        w = None if a[wname] is None else a[wname].double().requires_grad_(True)
+        want, z = define(xd, w, a["eps"], c, s, ia, ib)
+        want.backward(dy.double())
+        pair = z.detach().abs()
+        pair[..., ia], pair[..., ib] = pair[..., ia] + pair[..., ib], pair[..., ia] + pair[..., ib]
+        err = (y.double() - want.detach()).abs()
+        assert (err <= U * want.detach().abs() + 2.0 ** -16 * pair).all(), f"forward {wname}: {float(err.max())}"
+        # magnitudes of the backward's terms
+        back = dy.double().abs()
+        both = back.clone()
+        both[..., ia] = both[..., ib] = back[..., ia] + back[..., ib]
+        if w is None:
+            mag = both
+        else:
+            r = 1 / torch.sqrt((xd.detach() ** 2).mean(-1, keepdim=True) + a["eps"])
+            xhat = (xd.detach() * r).abs()
+            gw = both * w.detach().abs()
+            mag = r * (gw + xhat * (gw * xhat).mean(-1, keepdim=True))
+            sums = (both * xhat).sum((0, 1))
+            assert ((dw.double() - w.grad).abs() <= 2.0 ** -12 * sums + 1e-30).all(), f"gradient of {wname}"
+            assert float((dw.double() - w.grad).norm()) <= 2.0 ** -15 * float(sums.norm())
+        err = (dx.double() - xd.grad).abs()
+        assert (err <= U * xd.grad.abs() + 2.0 ** -14 * mag).all(), f"backward {wname}: {float(err.max())}"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_positions_over_the_whole_int32_range(interleaved):
+    """An fp32 angle would be off by whole turns here; the reference reduces the angle with integers:
+    inv_freq = m 2^-e exactly, so position * inv_freq is exact in Python integers."""
+    import math
+    from fractions import Fraction
+
+    import io_aware_exact_flash_gb300 as fa
+
+    T, d = 6, 64
+    q = torch.ones(T, 1, d, device="cuda", dtype=torch.bfloat16)
+    pos = torch.tensor([0, 1, -1, 2 ** 31 - 1, -2 ** 31, 1234567891], device="cuda", dtype=torch.int32)
+    inv = torch.logspace(0, -6, d // 2, dtype=torch.float64).float().cuda()
+    y, _ = fa.fa_qk_norm_rope(q, q, positions=pos, inv_freq=inv, interleaved=interleaved)
+    # pi to 150 bits (Machin's formula in rationals)
+    atan = lambda n: sum(Fraction((-1) ** i, (2 * i + 1) * n ** (2 * i + 1)) for i in range(40))  # noqa: E731
+    two_pi = 2 * (16 * atan(5) - 4 * atan(239))
+    for t in range(T):
+        for i in range(d // 2):
+            turn = Fraction(int(pos[t])) * Fraction(float(inv[i])) / two_pi
+            phi = 2 * math.pi * float(turn - (turn.numerator // turn.denominator))
+            a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + d // 2)
+            # fp64 rounding of inv_freq / 2 pi moves the turn by at most 2^31 2^-53 2, i.e. 3e-6 of an angle
+            for got, want in ((y[t, 0, a], math.cos(phi) - math.sin(phi)), (y[t, 0, b], math.cos(phi) + math.sin(phi))):
+                assert abs(float(got) - want) <= U * abs(want) + 1e-5
+
+
+@pytest.mark.gpu
+def test_in_place_and_strided_outputs():
+    import io_aware_exact_flash_gb300 as fa
+
+    T, Hq, Hkv, d = 37, 6, 2, 128
+    q, k, a, dyq, dyk = make(T, Hq, Hkv, d, d, 1, True, fused=True)
+    want = fa.fa_qk_norm_rope(q, k, **a)
+    wgrad = fa.fa_qk_norm_rope_bwd(dyq, dyk, q, k, **a)
+    qkv = q._base.clone()
+    values = qkv[:, (Hq + Hkv) * d:].clone()
+    q2 = qkv[:, :Hq * d].unflatten(1, (Hq, d))
+    k2 = qkv[:, Hq * d:(Hq + Hkv) * d].unflatten(1, (Hkv, d))
+    got = fa.fa_qk_norm_rope(q2, k2, q_out=q2, k_out=k2, **a)  # in place, inside the projection
+    assert got[0] is q2 and torch.equal(q2, want[0]) and torch.equal(k2, want[1])
+    assert torch.equal(qkv[:, (Hq + Hkv) * d:], values)
+    # gradients written into the projection's gradient; then in place over the incoming ones
+    dqkv = torch.full_like(qkv, float("nan"))
+    dq2 = dqkv[:, :Hq * d].unflatten(1, (Hq, d))
+    dk2 = dqkv[:, Hq * d:(Hq + Hkv) * d].unflatten(1, (Hkv, d))
+    fa.fa_qk_norm_rope_bwd(dyq, dyk, q, k, dq=dq2, dk=dk2, **a)
+    assert torch.equal(dq2, wgrad[0]) and torch.equal(dk2, wgrad[1])
+    assert torch.isnan(dqkv[:, (Hq + Hkv) * d:]).all()
+    g1, g2 = dyq.clone(), dyk.clone()
+    res = fa.fa_qk_norm_rope_bwd(g1, g2, q, k, dq=g1, dk=g2, **a)
+    assert all(torch.equal(x, y) for x, y in zip(res, wgrad))
+
+
+@pytest.mark.gpu
+def test_no_tokens():
+    import io_aware_exact_flash_gb300 as fa
+
+    q, k, a, dyq, dyk = make(0, 4, 2, 64, 64, 1, True)
+    out = fa.fa_qk_norm_rope(q, k, **a)
+    assert out[0].shape == (0, 4, 64) and out[1].shape == (0, 2, 64)
+    nan = torch.full((64,), float("nan"), device="cuda")
+    dq, dk, dwq, dwk = fa.fa_qk_norm_rope_bwd(dyq, dyk, q, k, dq_weight=nan, dk_weight=nan.clone(), **a)
+    assert dq.shape == q.shape and not dwq.any() and not dwk.any()
+
+
+@pytest.mark.gpu
+def test_zero_and_non_finite_heads_stay_apart():
+    """A head of zeros normalises to zeros (eps > 0), and a non-finite element reaches no other head."""
+    import io_aware_exact_flash_gb300 as fa
+
+    q, k, a, _, _ = make(9, 8, 2, 128, 128, 1, True)
+    clean = fa.fa_qk_norm_rope(q, k, **a)[0]
+    q = q.clone()
+    q[4, 3] = 0
+    q[5, 2, 7] = float("inf")
+    q[6, 1, 100] = float("nan")
+    y = fa.fa_qk_norm_rope(q, k, **a)[0]
+    assert not y[4, 3].any()
+    touched = torch.zeros(9, 8, dtype=torch.bool, device="cuda")
+    touched[4, 3] = touched[5, 2] = touched[6, 1] = True
+    assert torch.equal(y[~touched], clean[~touched])
+    assert torch.isnan(y[6, 1]).all()
