@@ -44,26 +44,37 @@ struct RopeParams {
   const float* inv_freq;     // [rot / 2]
   float* partial;            // backward with weights: [gridDim.x, 2, d] sums of the weights' gradients
   int64_t T;
-  int heads[2], passes[2];  // passes: warp steps that cover the heads of one token
+  int heads[2];
+  int steps[2];            // warp steps that cover the heads of one token
+  int parts[2], per_part[2];  // a token's steps are split over `parts` units of `per_part` each
+  int warps[2];            // warps that walk the queries' units, and the keys'
   int rot, section_end[kMaxAxes - 1];  // pairs [section_end[a - 1], section_end[a]) belong to axis a
-  int parts, per_part;     // a token's passes are split over `parts` warps, `per_part` each
   float eps;
 };
 
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-__device__ __forceinline__ void unpack8(uint4 v, float* f) {
+// Eight bf16 elements as four pairs of fp32 values, and back.
+__device__ __forceinline__ void unpack8(uint4 v, uint64_t* f) {
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf_lo(u[i]);
-    f[2 * i + 1] = bf_hi(u[i]);
-  }
+  for (int i = 0; i < 4; ++i) f[i] = f32x2(bf_lo(u[i]), bf_hi(u[i]));
 }
-__device__ __forceinline__ uint4 pack8(const float* f) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ uint4 pack8(const uint64_t* f) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    split_f32x2(f[i], a, b);
+    u[i] = pack_bf16x2(a, b);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+__device__ __forceinline__ float pair_sum(uint64_t v) {
+  float a, b;
+  split_f32x2(v, a, b);
+  return a + b;
 }
 
 // Sum over the kLanes lanes that share a head.
@@ -74,22 +85,114 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
+// One head's loads of a lane: 16 elements of x and, backward, of dy.
+struct RopeLoads {
+  uint4 x0, x1, g0, g1;
+};
+
+// Angles of the 8 pairs a lane holds, for both arrangements of pairs.
+template <bool INTERLEAVED>
+struct Angles {
+  uint64_t c[4], s[4], ns[4];  // cos, sin, -sin of pairs (2 t, 2 t + 1)
+  __device__ __forceinline__ void read(const float* cosines, const float* sines) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const float2 a = *reinterpret_cast<const float2*>(cosines + 2 * t);
+      const float2 b = *reinterpret_cast<const float2*>(sines + 2 * t);
+      c[t] = f32x2(a.x, a.y);
+      s[t] = f32x2(b.x, b.y);
+      ns[t] = f32x2(-b.x, -b.y);
+    }
+  }
+  // The lane's 16 elements (8 register pairs) turned by the angles, or back by them.
+  template <bool BACK>
+  __device__ __forceinline__ void turn(uint64_t* x) const {
+    if constexpr (!INTERLEAVED) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const uint64_t a = x[t], b = x[4 + t];
+        x[t] = fma_f32x2(a, c[t], mul_f32x2(b, BACK ? s[t] : ns[t]));
+        x[4 + t] = fma_f32x2(b, c[t], mul_f32x2(a, BACK ? ns[t] : s[t]));
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        float a, b, c0, c1, s0, s1;
+        split_f32x2(x[t], a, b);
+        split_f32x2(c[t >> 1], c0, c1);
+        split_f32x2(s[t >> 1], s0, s1);
+        const float cc = t & 1 ? c1 : c0;
+        const float ss = BACK ? -(t & 1 ? s1 : s0) : (t & 1 ? s1 : s0);
+        x[t] = f32x2(fmaf(a, cc, -b * ss), fmaf(b, cc, a * ss));
+      }
+    }
+  }
+};
+
+// Heads a warp takes per step: one group of kHeads, or (forward, which has the registers) two, so that
+// twice the bytes are in flight. Resident CTAs per SM.
+template <bool BWD>
+constexpr int kRopeGroups = BWD ? 1 : 2;
+constexpr int kRopeBlocksPerSm = 2;
+
 template <int D, bool BWD, bool NORM, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kLanes = D / 16;       // lanes per head
-  constexpr int kHeads = 32 / kLanes;  // heads per warp step
-  __shared__ float2 angles[kRopeWarps][D / 2];
+  constexpr int kHeads = 32 / kLanes;  // heads per group
+  constexpr int kGroups = kRopeGroups<BWD>;
+  constexpr int kStep = kGroups * kHeads * D;  // elements per step
+  __shared__ alignas(16) float cosines[kRopeWarps][D / 2], sines[kRopeWarps][D / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int j = lane % kLanes, head_of = lane / kLanes;
   // This lane's elements: two runs of 8. Split halves: run 0 of the first half of the rotated
   // elements, run 1 the partners in the second half (past them, 16 in a row); adjacent pairs: 16 in a row.
-  const int rot_lanes = p.rot / 16;
-  const bool rotated = j < rot_lanes;
+  const bool rotated = 16 * j < p.rot;
   int c0 = 16 * j, c1 = 16 * j + 8;
   if (!INTERLEAVED && rotated) {
     c0 = 8 * j;
     c1 = p.rot / 2 + 8 * j;
   }
+  // A warp walks units of the queries or of the keys, never both: it needs one weight and, backward,
+  // one set of sums (32 registers fewer).
+  const int id = blockIdx.x * kRopeWarps + warp;
+  const int kind = id >= p.warps[0];
+  const uint32_t stride = kind ? p.warps[1] : p.warps[0];
+  const int heads = kind ? p.heads[1] : p.heads[0];
+  const uint32_t steps = kind ? p.steps[1] : p.steps[0];
+  const uint32_t parts = kind ? p.parts[1] : p.parts[0], per_part = kind ? p.per_part[1] : p.per_part[0];
+  const uint16_t* src = (kind ? p.x[1] : p.x[0]) + head_of * D;
+  const uint16_t* dsrc = (kind ? p.dy[1] : p.dy[0]) + head_of * D;
+  uint16_t* dst = (kind ? p.out[1] : p.out[0]) + head_of * D;
+  const int64_t x_stride = kind ? p.x_stride[1] : p.x_stride[0];
+  const int64_t dy_stride = kind ? p.dy_stride[1] : p.dy_stride[0];
+  const int64_t out_stride = kind ? p.out_stride[1] : p.out_stride[0];
+  // (more than one part only with few tokens: units, and the next unit of any warp, fit 32 bits)
+  const uint32_t units = (uint32_t)p.T * parts;
+  uint32_t unit = kind ? id - p.warps[0] : id;
+  if (kind && id - p.warps[0] >= p.warps[1]) unit = units;  // beyond the last warp: nothing to do
+
+  RopeLoads next[kGroups];
+  auto load = [&](uint32_t t, uint32_t step) {
+    const uint16_t* at = src + ((int64_t)t * x_stride + step * kStep);
+    const uint16_t* dat = dsrc + ((int64_t)t * dy_stride + step * kStep);
+#pragma unroll
+    for (int y = 0; y < kGroups; ++y) {
+      RopeLoads& v = next[y];
+      v.x0 = v.x1 = v.g0 = v.g1 = make_uint4(0, 0, 0, 0);
+      if ((int)(step * kGroups + y) * kHeads + head_of < heads) {
+        if (NORM || !BWD) {
+          v.x0 = __ldcs(reinterpret_cast<const uint4*>(at + y * kHeads * D + c0));
+          v.x1 = __ldcs(reinterpret_cast<const uint4*>(at + y * kHeads * D + c1));
+        }
+        if constexpr (BWD) {
+          v.g0 = __ldcs(reinterpret_cast<const uint4*>(dat + y * kHeads * D + c0));
+          v.g1 = __ldcs(reinterpret_cast<const uint4*>(dat + y * kHeads * D + c1));
+        }
+      }
+    }
+  };
+  if (unit < units) load(unit / parts, unit % parts * per_part);
+
   // the pairs whose angles this lane computes: lane and lane + 32
   uint64_t turn[2] = {0, 0};
   int axis[2] = {0, 0};
@@ -103,147 +206,128 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
       for (int a = 0; a < kMaxAxes - 1; ++a) axis[x] += i >= p.section_end[a];
     }
   }
-  uint4 wv[2][2];  // the lane's weights
+  int32_t pos[2] = {0, 0};
+  auto load_positions = [&](uint32_t t) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      if (lane + 32 * x < p.rot / 2) pos[x] = p.positions[axis[x] * p.T + t];
+  };
+  if (unit < units) load_positions(unit / parts);
+  uint64_t w[8];  // the lane's weights
   if constexpr (NORM) {
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      wv[x][0] = *reinterpret_cast<const uint4*>(p.w[x] + c0);
-      wv[x][1] = *reinterpret_cast<const uint4*>(p.w[x] + c1);
-    }
+    const uint16_t* wp = kind ? p.w[1] : p.w[0];
+    unpack8(*reinterpret_cast<const uint4*>(wp + c0), w);
+    unpack8(*reinterpret_cast<const uint4*>(wp + c1), w + 4);
   }
-  float dw[2][16];  // backward: this lane's share of the weights' gradients
+  uint64_t dw[8];  // backward: this lane's share of the weight's gradient
 #pragma unroll
-  for (int i = 0; i < 16; ++i) dw[0][i] = dw[1][i] = 0.f;
+  for (int i = 0; i < 8; ++i) dw[i] = 0ull;
 
-  const int64_t units = p.T * p.parts, stride = (int64_t)gridDim.x * kRopeWarps;
-  for (int64_t unit = (int64_t)blockIdx.x * kRopeWarps + warp; unit < units; unit += stride) {
-    const int64_t t = unit / p.parts;
-    const int first = (int)(unit % p.parts) * p.per_part;
-    const int last = min(first + p.per_part, p.passes[0] + p.passes[1]);
-    float cs[8], sn[8];
+  for (; unit < units; unit += stride) {
+    const uint32_t t = unit / parts;
+    const uint32_t first = (unit - t * parts) * per_part, last = min(first + per_part, steps);
+    uint16_t* at = dst + ((int64_t)t * out_stride + first * kStep);
+    Angles<INTERLEAVED> ang;
     if (p.rot > 0) {
       __syncwarp();  // the previous token's angles have been read
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int i = lane + 32 * x;
         if (i < p.rot / 2) {
-          const int64_t pos = p.positions[axis[x] * p.T + t];
-          const int32_t turns = (int32_t)(((uint64_t)pos * turn[x]) >> 32);  // 2^-32 of a turn
-          float s, c;
-          sincospif((float)turns * 0x1p-31f, &s, &c);
-          angles[warp][i] = make_float2(c, s);
+          const int32_t turns = (int32_t)(((uint64_t)(int64_t)pos[x] * turn[x]) >> 32);  // 2^-32 of a turn
+          sincospif((float)turns * 0x1p-31f, &sines[warp][i], &cosines[warp][i]);
         }
       }
       __syncwarp();
-      if (rotated) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 a = angles[warp][8 * j + i];
-          cs[i] = a.x;
-          sn[i] = a.y;
-        }
-      }
+      if (rotated) ang.read(&cosines[warp][8 * j], &sines[warp][8 * j]);
+      if (unit + stride < units) load_positions((unit + stride) / parts);
     }
-#pragma unroll 2
-    for (int pass = first; pass < last; ++pass) {
-      const int which = pass >= p.passes[0];  // 0: queries, 1: keys
-      const int head = (pass - (which ? p.passes[0] : 0)) * kHeads + head_of;
-      const bool live = head < (which ? p.heads[1] : p.heads[0]);
-      const uint16_t* src = (which ? p.x[1] : p.x[0]) + t * (which ? p.x_stride[1] : p.x_stride[0]) + head * D;
-      const uint16_t* dsrc = (which ? p.dy[1] : p.dy[0]) + t * (which ? p.dy_stride[1] : p.dy_stride[0]) + head * D;
-      uint16_t* dst = (which ? p.out[1] : p.out[0]) + t * (which ? p.out_stride[1] : p.out_stride[0]) + head * D;
-      float x[16], g[16];
-      uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0, g0 = x0, g1 = x0;
-      if (live) {
+#pragma unroll 1
+    for (uint32_t step = first; step < last; ++step, at += kStep) {
+      RopeLoads cur[kGroups];
+#pragma unroll
+      for (int y = 0; y < kGroups; ++y) cur[y] = next[y];
+      // the next step's loads are on their way while this one is computed
+      if (step + 1 < last) {
+        load(t, step + 1);
+      } else if (unit + stride < units) {
+        const uint32_t u = unit + stride;
+        load(u / parts, u % parts * per_part);
+      }
+#pragma unroll
+      for (int y = 0; y < kGroups; ++y) {
+        const RopeLoads& v = cur[y];
+        uint64_t x[8];
+        float r = 1.f;
         if (NORM || !BWD) {
-          x0 = __ldcs(reinterpret_cast<const uint4*>(src + c0));
-          x1 = __ldcs(reinterpret_cast<const uint4*>(src + c1));
-        }
-        if constexpr (BWD) {
-          g0 = __ldcs(reinterpret_cast<const uint4*>(dsrc + c0));
-          g1 = __ldcs(reinterpret_cast<const uint4*>(dsrc + c1));
-        }
-      }
-      unpack8(x0, x);
-      unpack8(x1, x + 8);
-      float w[16], r = 1.f;
-      if constexpr (NORM) {
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
-        r = rsqrtf(head_sum<kLanes>(ss) * (1.f / D) + p.eps);
-        unpack8(which ? wv[1][0] : wv[0][0], w);
-        unpack8(which ? wv[1][1] : wv[0][1], w + 8);
-      }
-      if constexpr (!BWD) {
-        if constexpr (NORM) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = x[i] * r * w[i];
-        }
-        if (rotated) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float& a = x[INTERLEAVED ? 2 * i : i];
-            float& b = x[INTERLEAVED ? 2 * i + 1 : 8 + i];
-            const float a0 = a, b0 = b;
-            a = a0 * cs[i] - b0 * sn[i];
-            b = b0 * cs[i] + a0 * sn[i];
-          }
-        }
-      } else {
-        unpack8(g0, g);
-        unpack8(g1, g + 8);
-        if (rotated) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float& a = g[INTERLEAVED ? 2 * i : i];
-            float& b = g[INTERLEAVED ? 2 * i + 1 : 8 + i];
-            const float a0 = a, b0 = b;
-            a = a0 * cs[i] + b0 * sn[i];
-            b = b0 * cs[i] - a0 * sn[i];
-          }
+          unpack8(v.x0, x);
+          unpack8(v.x1, x + 4);
         }
         if constexpr (NORM) {
-          float inner = 0.f;
+          uint64_t ss = mul_f32x2(x[0], x[0]), ss1 = mul_f32x2(x[4], x[4]);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            x[i] *= r;
-            const float v = g[i] * x[i];
-            if (which) dw[1][i] += v;
-            else dw[0][i] += v;
-            inner = fmaf(v, w[i], inner);
+          for (int i = 1; i < 4; ++i) {
+            ss = fma_f32x2(x[i], x[i], ss);
+            ss1 = fma_f32x2(x[4 + i], x[4 + i], ss1);
           }
-          inner = head_sum<kLanes>(inner) * (1.f / D);
+          r = rsqrtf(head_sum<kLanes>(pair_sum(add_f32x2(ss, ss1))) * (1.f / D) + p.eps);
+        }
+        const uint64_t r2 = f32x2(r, r);
+        if constexpr (!BWD) {
+          if constexpr (NORM) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = (g[i] * w[i] - x[i] * inner) * r;
+            for (int i = 0; i < 8; ++i) x[i] = mul_f32x2(mul_f32x2(x[i], r2), w[i]);
+          }
+          if (rotated) ang.template turn<false>(x);
         } else {
+          uint64_t g[8];
+          unpack8(v.g0, g);
+          unpack8(v.g1, g + 4);
+          if (rotated) ang.template turn<true>(g);
+          if constexpr (NORM) {
+            uint64_t in0 = 0ull, in1 = 0ull;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = g[i];
+            for (int i = 0; i < 8; ++i) {
+              x[i] = mul_f32x2(x[i], r2);
+              const uint64_t gx = mul_f32x2(g[i], x[i]);
+              dw[i] = add_f32x2(dw[i], gx);
+              if (i & 1) in1 = fma_f32x2(gx, w[i], in1);
+              else in0 = fma_f32x2(gx, w[i], in0);
+            }
+            const float inner = head_sum<kLanes>(pair_sum(add_f32x2(in0, in1))) * (-1.f / D);
+            const uint64_t inner2 = f32x2(inner, inner);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = mul_f32x2(fma_f32x2(x[i], inner2, mul_f32x2(g[i], w[i])), r2);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = g[i];
+          }
         }
-      }
-      if (live) {
-        *reinterpret_cast<uint4*>(dst + c0) = pack8(x);
-        *reinterpret_cast<uint4*>(dst + c1) = pack8(x + 8);
+        if ((int)(step * kGroups + y) * kHeads + head_of < heads) {
+          *reinterpret_cast<uint4*>(at + y * kHeads * D + c0) = pack8(x);
+          *reinterpret_cast<uint4*>(at + y * kHeads * D + c1) = pack8(x + 4);
+        }
       }
     }
   }
   if constexpr (BWD && NORM) {
     // heads of the warp, then warps of the CTA, in a fixed order; one row of partial sums per CTA
-    __shared__ float sums[kRopeWarps][2][D];
+    __shared__ float sums[kRopeWarps][D];
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int i = 0; i < 16; ++i) {
+      float lo, hi;
+      split_f32x2(dw[i >> 1], lo, hi);
+      float v = i & 1 ? hi : lo;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float v = dw[x][i];
-#pragma unroll
-        for (int o = 16; o >= kLanes; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (head_of == 0) sums[warp][x][(i < 8 ? c0 : c1 - 8) + i] = v;
-      }
+      for (int o = 16; o >= kLanes; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (head_of == 0) sums[warp][(i < 8 ? c0 : c1 - 8) + i] = v;
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * D; i += kRopeThreads) {
       float v = 0.f;
 #pragma unroll
-      for (int k = 0; k < kRopeWarps; ++k) v += sums[k][i / D][i % D];
+      for (int k = 0; k < kRopeWarps; ++k)
+        if ((int)(blockIdx.x * kRopeWarps + k >= p.warps[0]) == i / D) v += sums[k][i % D];
       p.partial[(int64_t)blockIdx.x * 2 * D + i] = v;
     }
   }
@@ -253,6 +337,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 // take every 8th row each, and are added in order.
 __global__ void __launch_bounds__(256) rope_weight_grad_kernel(const float* partial, int rows, int d, float* dq_weight,
                                                                float* dk_weight) {
+  griddep_wait();  // launched while the kernel that writes `partial` finishes
   __shared__ float sums[8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
   float v = 0.f;
@@ -268,28 +353,36 @@ __global__ void __launch_bounds__(256) rope_weight_grad_kernel(const float* part
   }
 }
 
-// Warps per SM that the kernel is spread over.
-constexpr int kRopeWarpsPerSm = 32;
+// With tokens enough to fill the GPU, the queries' and the keys' warps are in proportion to their steps
+// and a token's steps of one kind stay in one warp (its angles are computed once); with few tokens they
+// are spread over more warps, down to one step each. Returns the number of CTAs.
+int split_rope(RopeParams& p, int64_t T, int sm_count) {
+  const int total = p.steps[0] + p.steps[1];
+  const int64_t most = (int64_t)sm_count * kRopeBlocksPerSm * kRopeWarps;
+  const int64_t per_token = T > 0 ? most / T : 1;  // warps there are for each token
+  int64_t want[2];
+  for (int x = 0; x < 2; ++x) {
+    int64_t parts = per_token * p.steps[x] / total;
+    parts = parts < 1 ? 1 : parts > p.steps[x] ? p.steps[x] : parts;
+    p.per_part[x] = (int)((p.steps[x] + parts - 1) / parts);
+    p.parts[x] = (p.steps[x] + p.per_part[x] - 1) / p.per_part[x];
+    want[x] = T * p.parts[x];
+  }
+  if (want[0] + want[1] > most) {
+    int64_t queries = (most * p.steps[0] + total / 2) / total;
+    queries = queries < 1 ? 1 : queries > most - 1 ? most - 1 : queries;
+    want[1] = want[1] < most - queries ? want[1] : most - queries;
+    want[0] = want[0] < most - want[1] ? want[0] : most - want[1];
+  }
+  p.warps[0] = (int)want[0];
+  p.warps[1] = (int)want[1];
+  return (int)((want[0] + want[1] + kRopeWarps - 1) / kRopeWarps);
+}
 
-int rope_max_blocks(int sm_count) { return sm_count * kRopeWarpsPerSm / kRopeWarps; }
-
-struct RopeSplit {
-  int parts, per_part, blocks;
-};
-
-// A token's passes stay in one warp when there are tokens enough to fill the GPU (its angles are then
-// computed once); with few tokens they are spread over more warps, down to one pass each.
-RopeSplit split_rope(int64_t T, int passes, int sm_count) {
-  RopeSplit s;
-  const int64_t target = (int64_t)sm_count * kRopeWarpsPerSm;
-  int64_t parts = T > 0 ? (target + T - 1) / T : 1;
-  if (parts > passes) parts = passes;
-  if (parts < 1) parts = 1;
-  s.per_part = (int)((passes + parts - 1) / parts);
-  s.parts = (passes + s.per_part - 1) / s.per_part;
-  const int64_t blocks = (T * s.parts + kRopeWarps - 1) / kRopeWarps;
-  s.blocks = (int)(blocks < rope_max_blocks(sm_count) ? blocks : rope_max_blocks(sm_count));
-  return s;
+void set_steps(RopeParams& p, int Hq, int Hkv, int d, bool bwd) {
+  const int per_step = 32 / (d / 16) * (bwd ? kRopeGroups<true> : kRopeGroups<false>);
+  p.steps[0] = (Hq + per_step - 1) / per_step;
+  p.steps[1] = (Hkv + per_step - 1) / per_step;
 }
 
 template <int D, bool BWD>
@@ -302,6 +395,21 @@ cudaError_t launch_rope(const RopeParams& p, int blocks, bool norm, bool interle
     else rope_kernel<D, BWD, false, false><<<blocks, kRopeThreads, 0, stream>>>(p);
   }
   return cudaGetLastError();
+}
+
+cudaError_t launch_weight_grad(const float* partial, int rows, int d, float* dq_weight, float* dk_weight,
+                               cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * d / 32));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, rope_weight_grad_kernel, partial, rows, d, dq_weight, dk_weight);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 // One [T, heads, d] tensor of a call: rows of heads * d elements, `stride` elements apart.
@@ -361,9 +469,6 @@ fa_status rope_setup(RopeParams& p, const void* q_weight, const void* k_weight, 
   p.T = T;
   p.heads[0] = Hq;
   p.heads[1] = Hkv;
-  const int per_pass = 32 / (d / 16);
-  p.passes[0] = (Hq + per_pass - 1) / per_pass;
-  p.passes[1] = (Hkv + per_pass - 1) / per_pass;
   p.rot = rot_dim;
   p.eps = eps;
   return FA_OK;
@@ -413,12 +518,11 @@ extern "C" fa_status fa_qk_norm_rope(const void* q, int64_t q_stride, const void
   const int rc = fa::current_device_info(&status, &sm_count);
   if (rc != FA_OK) return (fa_status)rc;
   if (T == 0) return FA_OK;
-  const fa::RopeSplit s = fa::split_rope(T, p.passes[0] + p.passes[1], sm_count);
-  p.parts = s.parts;
-  p.per_part = s.per_part;
+  fa::set_steps(p, Hq, Hkv, d, false);
+  const int blocks = fa::split_rope(p, T, sm_count);
   const bool norm = q_weight != nullptr;
-  const cudaError_t e = d == 128 ? fa::launch_rope<128, false>(p, s.blocks, norm, interleaved != 0, stream)
-                                 : fa::launch_rope<64, false>(p, s.blocks, norm, interleaved != 0, stream);
+  const cudaError_t e = d == 128 ? fa::launch_rope<128, false>(p, blocks, norm, interleaved != 0, stream)
+                                 : fa::launch_rope<64, false>(p, blocks, norm, interleaved != 0, stream);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -428,10 +532,10 @@ extern "C" size_t fa_qk_norm_rope_bwd_workspace_bytes(int64_t T, int Hq, int Hkv
   int sm_count = 152;  // without a device the size is that of a full part
   fa::current_device_info(&status, &sm_count);
   if (sm_count <= 0) sm_count = 152;
-  const int per_pass = 32 / (d / 16);
-  const int64_t passes = ((int64_t)Hq + per_pass - 1) / per_pass + ((int64_t)Hkv + per_pass - 1) / per_pass;
-  if (passes > (1 << 20)) return 0;
-  return (size_t)fa::split_rope(T, (int)passes, sm_count).blocks * 2 * d * sizeof(float);
+  if ((int64_t)Hq + Hkv > (1 << 20)) return 0;
+  fa::RopeParams p;
+  fa::set_steps(p, Hq, Hkv, d, true);
+  return (size_t)fa::split_rope(p, T, sm_count) * 2 * d * sizeof(float);
 }
 
 extern "C" fa_status fa_qk_norm_rope_bwd(const void* dq_out, int64_t dq_out_stride, const void* dk_out,
@@ -470,19 +574,18 @@ extern "C" fa_status fa_qk_norm_rope_bwd(const void* dq_out, int64_t dq_out_stri
   int sm_count = 0;
   const int rc = fa::current_device_info(&status, &sm_count);
   if (rc != FA_OK) return (fa_status)rc;
-  const fa::RopeSplit s = fa::split_rope(T, p.passes[0] + p.passes[1], sm_count);
-  const size_t need = norm ? (size_t)s.blocks * 2 * d * sizeof(float) : 0;
+  fa::set_steps(p, Hq, Hkv, d, true);
+  const int blocks = fa::split_rope(p, T, sm_count);
+  const size_t need = norm ? (size_t)blocks * 2 * d * sizeof(float) : 0;
   if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_WORKSPACE;
   if (need > 0 && !fa::is_aligned(workspace, 256)) return FA_ERR_ALIGNMENT;
-  p.parts = s.parts;
-  p.per_part = s.per_part;
   p.partial = static_cast<float*>(workspace);
   if (T > 0) {
-    const cudaError_t e = d == 128 ? fa::launch_rope<128, true>(p, s.blocks, norm, interleaved != 0, stream)
-                                   : fa::launch_rope<64, true>(p, s.blocks, norm, interleaved != 0, stream);
+    const cudaError_t e = d == 128 ? fa::launch_rope<128, true>(p, blocks, norm, interleaved != 0, stream)
+                                   : fa::launch_rope<64, true>(p, blocks, norm, interleaved != 0, stream);
     if (e != cudaSuccess) return FA_ERR_CUDA;
   }
   if (!norm) return FA_OK;
-  fa::rope_weight_grad_kernel<<<2 * d / 32, 256, 0, stream>>>(p.partial, s.blocks, d, dq_weight, dk_weight);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return fa::launch_weight_grad(p.partial, blocks, d, dq_weight, dk_weight, stream) == cudaSuccess ? FA_OK
+                                                                                                   : FA_ERR_CUDA;
 }
