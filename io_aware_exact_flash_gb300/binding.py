@@ -172,41 +172,55 @@ def fa_fwd(q, k, v, causal=False, scale=None, out=None, lse=None, return_lse=Tru
     return out, lse
 
 
-def _one_device(like, tensors):
+# The functions below are called for small tensors too, where the host's time counts: addresses go to
+# ctypes as plain integers, and a call on the current device enters no context.
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _one_device(index, tensors):
     """Every tensor of a call lives on one device (None entries are absent arguments)."""
     for name, t in tensors:
-        if t is not None and t.device != like.device:
-            raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
 
 
-def _on_device(device, stream):
-    """Context of a call: `device` is current, and allocations belong to `stream` (default: that
+_NO_CONTEXT = contextlib.nullcontext()
+
+
+def _on_device(index, stream):
+    """Context of a call: device `index` is current, and allocations belong to `stream` (default: that
     device's current stream)."""
     if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        if stream.device.index != index:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
         return torch.cuda.stream(stream)  # makes its device current too
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    if index == torch.cuda.current_device():
+        return _NO_CONTEXT
+    return torch.cuda.device(index)
 
 
-def _result(name, t, shape, dtype, device):
+def _handle(index, stream):
+    """The CUDA stream a call runs on, as an integer."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def _result(name, t, like_shape, dtype, index):
     """A caller-given output after its checks, or a new one."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape)
+        return torch.empty(like_shape, dtype=dtype, device=torch.device("cuda", index))
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.get_device() != index or t.shape != like_shape
             or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(like_shape)} on cuda:{index}")
     return t
 
 
-def _scratch(workspace, need, device):
+def _scratch(workspace, need, index):
     """A caller-given workspace (any contiguous CUDA tensor), or a new one; with its size in bytes."""
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    elif not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        workspace = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
+    elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -236,17 +250,19 @@ def fa_bwd(q, k, v, out, lse, dout, causal=False, scale=None, dlse=None, dq=None
         if (not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_cuda or t.shape != (B, S, Hq)
                 or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of shape {(B, S, Hq)}")
-    _one_device(q, (("k", k), ("v", v), ("out", out), ("lse", lse), ("dout", dout), ("dlse", dlse)))
+    index = q.get_device()
+    _one_device(index, (("k", k), ("v", v), ("out", out), ("lse", lse), ("dout", dout), ("dlse", dlse)))
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     lib = load_library()
-    with _on_device(q.device, stream):
-        dq = _result("dq", dq, q.shape, q.dtype, q.device)
-        dk = _result("dk", dk, k.shape, k.dtype, q.device)
-        dv = _result("dv", dv, v.shape, v.dtype, q.device)
-        workspace, ws_bytes = _scratch(workspace, fa_bwd_workspace_bytes(B, Hq, Hkv, S, d, causal), q.device)
-        code = lib.fa_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dlse), _ptr(dq), _ptr(dk),
-                          _ptr(dv), B, Hq, Hkv, S, d, int(bool(causal)), scale, _ptr(workspace), ws_bytes,
-                          _stream(stream))
+    with _on_device(index, stream):
+        dq = _result("dq", dq, q.shape, q.dtype, index)
+        dk = _result("dk", dk, k.shape, k.dtype, index)
+        dv = _result("dv", dv, v.shape, v.dtype, index)
+        need = 0 if workspace is not None else fa_bwd_workspace_bytes(B, Hq, Hkv, S, d, causal)
+        workspace, ws_bytes = _scratch(workspace, need, index)
+        code = lib.fa_bwd(_address(q), _address(k), _address(v), _address(out), _address(lse), _address(dout),
+                          _address(dlse), _address(dq), _address(dk), _address(dv), B, Hq, Hkv, S, d,
+                          int(bool(causal)), scale, _address(workspace), ws_bytes, _handle(index, stream))
     _check("fa_bwd", code)
     return dq, dk, dv
 
@@ -405,57 +421,59 @@ def fa_paged_append(k_new, v_new, cu_seqlens_new, kv_lens_before, page_table, k_
     _check("fa_paged_append", code)
 
 
-def _token_rows(name, t, shape=None, device=None):
-    """A [T, heads, d] bf16 CUDA tensor whose heads are contiguous within a token (a view of a fused
-    projection, for instance); returns its token stride in elements."""
+def _token_rows(name, t, shape=None, index=None):
+    """Checks a [T, heads, d] bf16 CUDA tensor whose heads are contiguous within a token (a view of a
+    fused projection, for instance); returns its token stride in elements."""
     if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA bfloat16 tensor")
-    if t.dim() != 3 or (shape is not None and t.shape != shape):
-        raise ValueError(f"{name} must be [T, heads, d]" + (f" = {tuple(shape)}" if shape is not None else ""))
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be of shape {tuple(shape)}")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T, heads, d]")
     T, H, d = t.shape
     s_t, s_h, s_d = t.stride()
-    if T == 0:
-        return H * d
-    if (d > 1 and s_d != 1) or (H > 1 and s_h != d):
+    if T > 0 and ((d > 1 and s_d != 1) or (H > 1 and s_h != d)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     return s_t if T > 1 else H * d
 
 
-def _rope_arguments(q, k, positions, inv_freq, q_weight, k_weight, sections):
-    """The arguments that fa_qk_norm_rope and its backward share, checked: (positions, inv_freq,
-    num_axes, sections as a host array, rot_dim)."""
-    T, d, device = q.shape[0], q.shape[2], q.device
+def _rope_arguments(q, k, index, positions, inv_freq, q_weight, k_weight, sections):
+    """Checks the arguments that fa_qk_norm_rope and its backward share; returns (num_axes, sections as a
+    host array, rot_dim)."""
+    T, _, d = q.shape
     if k.shape[0] != T or k.shape[2] != d:
         raise ValueError("q and k must be [T, Hq, d] and [T, Hkv, d]")
     if (q_weight is None) != (k_weight is None):
         raise ValueError("q_weight and k_weight go together")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None and (w.dtype != torch.bfloat16 or w.shape != (d,) or w.device != device
-                              or not w.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous bfloat16 tensor of {d} elements on {device}")
+    if q_weight is not None:
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w.dtype != torch.bfloat16 or w.shape != (d,) or w.get_device() != index or not w.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous bfloat16 tensor of {d} elements on cuda:{index}")
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq go together")
     if positions is None:
         if q_weight is None:
             raise ValueError("nothing to do: neither weights nor positions")
         return 1, None, 0
-    if (inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or inv_freq.device != device
+    if (inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or inv_freq.get_device() != index
             or not inv_freq.is_contiguous()):
-        raise ValueError(f"inv_freq must be a contiguous 1-D float32 tensor on {device}")
-    num_axes = 1 if positions.dim() == 1 else positions.shape[0]
-    if (positions.dtype != torch.int32 or positions.dim() not in (1, 2) or positions.shape[-1] != T
-            or positions.device != device or not positions.is_contiguous()):
-        raise ValueError(f"positions must be a contiguous int32 tensor [T] or [axes, T] on {device}, T = {T}")
+        raise ValueError(f"inv_freq must be a contiguous 1-D float32 tensor on cuda:{index}")
+    axes_of = positions.dim()
+    if (positions.dtype != torch.int32 or axes_of not in (1, 2) or positions.shape[-1] != T
+            or positions.get_device() != index or not positions.is_contiguous()):
+        raise ValueError(f"positions must be a contiguous int32 tensor [T] or [axes, T] on cuda:{index}, T = {T}")
+    num_axes = 1 if axes_of == 1 else positions.shape[0]
     pairs = inv_freq.shape[0]
     if sections is None:
         if num_axes != 1:
             raise ValueError("sections must give the pairs of each position axis")
-        return num_axes, None, 2 * pairs
-    if len(sections) != num_axes or sum(sections) != pairs:
+    elif len(sections) != num_axes or sum(sections) != pairs or min(sections) < 0:
         raise ValueError(f"sections must be {num_axes} counts that add up to {pairs}")
-    return num_axes, (ctypes.c_int32 * num_axes)(*sections), 2 * pairs
+    elif num_axes > 1:
+        return num_axes, (ctypes.c_int32 * num_axes)(*sections), 2 * pairs
+    return num_axes, None, 2 * pairs
 
 
 def fa_qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6, sections=None,
@@ -468,20 +486,22 @@ def fa_qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight
     [pairs] fp32, where 2 * pairs elements of each head are rotated; both None: norm only.
     interleaved: pairs are (2i, 2i + 1) instead of (i, i + pairs). q_out may be q and k_out k (in
     place). Returns (q_out, k_out)."""
-    sq, sk = _token_rows("q", q), _token_rows("k", k, device=q.device)
-    num_axes, host_sections, rot_dim = _rope_arguments(q, k, positions, inv_freq, q_weight, k_weight, sections)
+    sq = _token_rows("q", q)
+    index = q.get_device()
+    sk = _token_rows("k", k, None, index)
+    num_axes, host_sections, rot_dim = _rope_arguments(q, k, index, positions, inv_freq, q_weight, k_weight, sections)
     T, Hq, d = q.shape
     lib = load_library()
-    with _on_device(q.device, stream):
+    with _on_device(index, stream):
         if q_out is None:
             q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         if k_out is None:
             k_out = torch.empty(k.shape, dtype=k.dtype, device=q.device)
-        so, sp = _token_rows("q_out", q_out, q.shape, q.device), _token_rows("k_out", k_out, k.shape, q.device)
-        code = lib.fa_qk_norm_rope(_ptr(q), sq, _ptr(k), sk, _ptr(q_weight), _ptr(k_weight), float(eps),
-                                   _ptr(positions), _ptr(inv_freq), num_axes, host_sections, rot_dim,
-                                   int(bool(interleaved)), T, Hq, k.shape[1], d, _ptr(q_out), so, _ptr(k_out), sp,
-                                   _stream(stream))
+        so, sp = _token_rows("q_out", q_out, q.shape, index), _token_rows("k_out", k_out, k.shape, index)
+        code = lib.fa_qk_norm_rope(_address(q), sq, _address(k), sk, _address(q_weight), _address(k_weight), eps,
+                                   _address(positions), _address(inv_freq), num_axes, host_sections, rot_dim,
+                                   int(bool(interleaved)), T, Hq, k.shape[1], d, _address(q_out), so,
+                                   _address(k_out), sp, _handle(index, stream))
     _check("fa_qk_norm_rope", code)
     return q_out, k_out
 
@@ -496,29 +516,33 @@ def fa_qk_norm_rope_bwd(dq_out, dk_out, q, k, positions=None, inv_freq=None, q_w
     """Gradients of fa_qk_norm_rope: dq_out, dk_out are those of its results, q and k its inputs (not
     read without weights). Returns (dq, dk, dq_weight, dk_weight): bf16 like q and k, and fp32 [d]
     (None without weights). dq may be dq_out and dk dk_out (in place)."""
-    sq, sk = _token_rows("q", q), _token_rows("k", k, device=q.device)
-    sg, sh = _token_rows("dq_out", dq_out, q.shape, q.device), _token_rows("dk_out", dk_out, k.shape, q.device)
-    num_axes, host_sections, rot_dim = _rope_arguments(q, k, positions, inv_freq, q_weight, k_weight, sections)
+    sq = _token_rows("q", q)
+    index = q.get_device()
+    sk = _token_rows("k", k, None, index)
+    sg, sh = _token_rows("dq_out", dq_out, q.shape, index), _token_rows("dk_out", dk_out, k.shape, index)
+    num_axes, host_sections, rot_dim = _rope_arguments(q, k, index, positions, inv_freq, q_weight, k_weight, sections)
     T, Hq, d = q.shape
+    Hkv = k.shape[1]
     lib = load_library()
-    with _on_device(q.device, stream):
+    with _on_device(index, stream):
         if dq is None:
             dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         if dk is None:
             dk = torch.empty(k.shape, dtype=k.dtype, device=q.device)
-        so, sp = _token_rows("dq", dq, q.shape, q.device), _token_rows("dk", dk, k.shape, q.device)
+        so, sp = _token_rows("dq", dq, q.shape, index), _token_rows("dk", dk, k.shape, index)
         ws_bytes = 0
         if q_weight is not None:
-            dq_weight = _result("dq_weight", dq_weight, (d,), torch.float32, q.device)
-            dk_weight = _result("dk_weight", dk_weight, (d,), torch.float32, q.device)
-            workspace, ws_bytes = _scratch(workspace, fa_qk_norm_rope_bwd_workspace_bytes(T, Hq, k.shape[1], d), q.device)
+            dq_weight = _result("dq_weight", dq_weight, q_weight.shape, torch.float32, index)
+            dk_weight = _result("dk_weight", dk_weight, k_weight.shape, torch.float32, index)
+            need = 0 if workspace is not None else fa_qk_norm_rope_bwd_workspace_bytes(T, Hq, Hkv, d)
+            workspace, ws_bytes = _scratch(workspace, need, index)
         else:
             dq_weight = dk_weight = workspace = None
-        code = lib.fa_qk_norm_rope_bwd(_ptr(dq_out), sg, _ptr(dk_out), sh, _ptr(q), sq, _ptr(k), sk, _ptr(q_weight),
-                                       _ptr(k_weight), float(eps), _ptr(positions), _ptr(inv_freq), num_axes,
-                                       host_sections, rot_dim, int(bool(interleaved)), T, Hq, k.shape[1], d, _ptr(dq),
-                                       so, _ptr(dk), sp, _ptr(dq_weight), _ptr(dk_weight), _ptr(workspace), ws_bytes,
-                                       _stream(stream))
+        code = lib.fa_qk_norm_rope_bwd(_address(dq_out), sg, _address(dk_out), sh, _address(q), sq, _address(k), sk,
+                                       _address(q_weight), _address(k_weight), eps, _address(positions),
+                                       _address(inv_freq), num_axes, host_sections, rot_dim, int(bool(interleaved)), T,
+                                       Hq, Hkv, d, _address(dq), so, _address(dk), sp, _address(dq_weight),
+                                       _address(dk_weight), _address(workspace), ws_bytes, _handle(index, stream))
     _check("fa_qk_norm_rope_bwd", code)
     return dq, dk, dq_weight, dk_weight
 

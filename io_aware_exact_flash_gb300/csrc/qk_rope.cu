@@ -19,6 +19,7 @@
 // a fraction of 2^64 once per thread (in fp64), and position times fraction mod 2^64 is exact.
 // Norms, weights' gradients and products are fp32; a result is rounded to bf16 once, at the end.
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -50,6 +51,7 @@ struct RopeParams {
   int warps[2];            // warps that walk the queries' units, and the keys'
   int rot, section_end[kMaxAxes - 1];  // pairs [section_end[a - 1], section_end[a]) belong to axis a
   float eps;
+  DeviceStatus* status;
 };
 
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
@@ -84,11 +86,6 @@ __device__ __forceinline__ float head_sum(float v) {
   for (int o = kLanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-
-// One head's loads of a lane: 16 elements of x and, backward, of dy.
-struct RopeLoads {
-  uint4 x0, x1, g0, g1;
-};
 
 // Angles of the 8 pairs a lane holds, for both arrangements of pairs.
 template <bool INTERLEAVED>
@@ -129,18 +126,33 @@ struct Angles {
   }
 };
 
-// Heads a warp takes per step: one group of kHeads, or (forward, which has the registers) two, so that
-// twice the bytes are in flight. Resident CTAs per SM.
-template <bool BWD>
-constexpr int kRopeGroups = BWD ? 1 : 2;
-constexpr int kRopeBlocksPerSm = 2;
+// Groups of heads a warp takes per step, resident CTAs per SM, and the steps' loads each warp keeps in
+// flight. The heads of a step are contiguous in memory, so one bulk copy brings them to shared memory
+// (and one more the gradients); registers could hold one step ahead at most.
+template <bool BWD, bool NORM>
+struct RopeTune {
+  static constexpr int kGroups = BWD && NORM ? 1 : 2;
+  static constexpr int kBlocks = 2;
+  static constexpr int kStages = 3;
+  static constexpr int kTensors = BWD && NORM ? 2 : 1;
+  // 16 bytes per lane and run: a group of heads is 1 KB, whatever d
+  static constexpr int kStageBytes = 1024 * kGroups * kTensors;
+  static constexpr int kSmemBytes = kRopeWarps * kStages * kStageBytes;
+};
+
+enum : uint32_t { kSiteRopeLoad = 50, kSiteRopeDrain = 51 };
 
 template <int D, bool BWD, bool NORM, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, (RopeTune<BWD, NORM>::kBlocks))
+    rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kLanes = D / 16;       // lanes per head
   constexpr int kHeads = 32 / kLanes;  // heads per group
-  constexpr int kGroups = kRopeGroups<BWD>;
+  constexpr int kGroups = RopeTune<BWD, NORM>::kGroups, kStages = RopeTune<BWD, NORM>::kStages;
+  constexpr int kTensors = RopeTune<BWD, NORM>::kTensors, kStageBytes = RopeTune<BWD, NORM>::kStageBytes;
   constexpr int kStep = kGroups * kHeads * D;  // elements per step
+  extern __shared__ __align__(128) uint8_t rope_smem[];  // [kRopeWarps][kStages]: x, then dy
+  __shared__ uint64_t loaded[kRopeWarps][kStages];
+  __shared__ int abort_flag;
   __shared__ alignas(16) float cosines[kRopeWarps][D / 2], sines[kRopeWarps][D / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int j = lane % kLanes, head_of = lane / kLanes;
@@ -160,8 +172,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_kernel(co
   const int heads = kind ? p.heads[1] : p.heads[0];
   const uint32_t steps = kind ? p.steps[1] : p.steps[0];
   const uint32_t parts = kind ? p.parts[1] : p.parts[0], per_part = kind ? p.per_part[1] : p.per_part[0];
-  const uint16_t* src = (kind ? p.x[1] : p.x[0]) + head_of * D;
-  const uint16_t* dsrc = (kind ? p.dy[1] : p.dy[0]) + head_of * D;
+  const uint16_t* src = kind ? p.x[1] : p.x[0];
+  const uint16_t* dsrc = kind ? p.dy[1] : p.dy[0];
   uint16_t* dst = (kind ? p.out[1] : p.out[0]) + head_of * D;
   const int64_t x_stride = kind ? p.x_stride[1] : p.x_stride[0];
   const int64_t dy_stride = kind ? p.dy_stride[1] : p.dy_stride[0];
@@ -171,27 +183,46 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_kernel(co
   uint32_t unit = kind ? id - p.warps[0] : id;
   if (kind && id - p.warps[0] >= p.warps[1]) unit = units;  // beyond the last warp: nothing to do
 
-  RopeLoads next[kGroups];
-  auto load = [&](uint32_t t, uint32_t step) {
-    const uint16_t* at = src + ((int64_t)t * x_stride + step * kStep);
-    const uint16_t* dat = dsrc + ((int64_t)t * dy_stride + step * kStep);
+  if (threadIdx.x == 0) abort_flag = 0;
+  if (lane == 0) {
 #pragma unroll
-    for (int y = 0; y < kGroups; ++y) {
-      RopeLoads& v = next[y];
-      v.x0 = v.x1 = v.g0 = v.g1 = make_uint4(0, 0, 0, 0);
-      if ((int)(step * kGroups + y) * kHeads + head_of < heads) {
-        if (NORM || !BWD) {
-          v.x0 = __ldcs(reinterpret_cast<const uint4*>(at + y * kHeads * D + c0));
-          v.x1 = __ldcs(reinterpret_cast<const uint4*>(at + y * kHeads * D + c1));
-        }
-        if constexpr (BWD) {
-          v.g0 = __ldcs(reinterpret_cast<const uint4*>(dat + y * kHeads * D + c0));
-          v.g1 = __ldcs(reinterpret_cast<const uint4*>(dat + y * kHeads * D + c1));
-        }
-      }
-    }
+    for (int i = 0; i < kStages; ++i) mbar_init(&loaded[warp][i], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  volatile int* abort = &abort_flag;
+  uint8_t* const staged = rope_smem + warp * (kStages * kStageBytes);
+  // Lane 0 loads kStages - 1 steps ahead of the arithmetic, over the units' ends. The lines are marked as
+  // the first to leave L2: they are read once, and the results, which are read next, should stay.
+  const uint64_t policy = policy_evict_first();
+  uint32_t ahead = unit, a_step = 0, a_last = 0, a_count = 0;
+  const uint16_t *a_src = src, *a_dsrc = dsrc;
+  auto enter = [&]() {  // the unit that is now ahead
+    const uint32_t t = ahead / parts;
+    a_step = (ahead - t * parts) * per_part;
+    a_last = min(a_step + per_part, steps);
+    a_src = src + ((int64_t)t * x_stride + a_step * kStep);
+    a_dsrc = dsrc + ((int64_t)t * dy_stride + a_step * kStep);
   };
-  if (unit < units) load(unit / parts, unit % parts * per_part);
+  auto load_ahead = [&]() {
+    if (ahead >= units) return;
+    const int s = a_count % kStages;
+    uint8_t* stage = staged + s * kStageBytes;
+    const uint32_t bytes = min(kGroups * kHeads, heads - (int)a_step * kGroups * kHeads) * D * 2;
+    mbar_arrive_expect_tx(&loaded[warp][s], kTensors * bytes);
+    if constexpr (NORM || !BWD) bulk_load_hint(stage, a_src, bytes, &loaded[warp][s], policy);
+    if constexpr (BWD) bulk_load_hint(stage + (kTensors - 1) * 1024 * kGroups, a_dsrc, bytes, &loaded[warp][s], policy);
+    ++a_count;
+    a_src += kStep;
+    a_dsrc += kStep;
+    if (++a_step == a_last && (ahead += stride) < units) enter();
+  };
+  if (lane == 0 && ahead < units) {
+    enter();
+#pragma unroll 1
+    for (int i = 0; i < kStages - 1; ++i) load_ahead();
+  }
+  uint32_t count = 0;  // steps computed
 
   // the pairs whose angles this lane computes: lane and lane + 32
   uint64_t turn[2] = {0, 0};
@@ -244,24 +275,20 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_kernel(co
     }
 #pragma unroll 1
     for (uint32_t step = first; step < last; ++step, at += kStep) {
-      RopeLoads cur[kGroups];
-#pragma unroll
-      for (int y = 0; y < kGroups; ++y) cur[y] = next[y];
-      // the next step's loads are on their way while this one is computed
-      if (step + 1 < last) {
-        load(t, step + 1);
-      } else if (unit + stride < units) {
-        const uint32_t u = unit + stride;
-        load(u / parts, u % parts * per_part);
-      }
+      __syncwarp();  // every lane has read the stage that is loaded next
+      if (lane == 0) load_ahead();
+      mbar_wait(&loaded[warp][count % kStages], (count / kStages) & 1, abort, p.status, kSiteRopeLoad);
+      const uint8_t* stage = staged + (count % kStages) * kStageBytes + head_of * D * 2;
+      ++count;
 #pragma unroll
       for (int y = 0; y < kGroups; ++y) {
-        const RopeLoads& v = cur[y];
+        // (a group past the last head computes on what the stage held before, and stores nothing)
+        const bool live = (int)(step * kGroups + y) * kHeads + head_of < heads;
         uint64_t x[8];
         float r = 1.f;
-        if (NORM || !BWD) {
-          unpack8(v.x0, x);
-          unpack8(v.x1, x + 4);
+        if constexpr (NORM || !BWD) {
+          unpack8(*reinterpret_cast<const uint4*>(stage + 1024 * y + 2 * c0), x);
+          unpack8(*reinterpret_cast<const uint4*>(stage + 1024 * y + 2 * c1), x + 4);
         }
         if constexpr (NORM) {
           uint64_t ss = mul_f32x2(x[0], x[0]), ss1 = mul_f32x2(x[4], x[4]);
@@ -281,8 +308,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_kernel(co
           if (rotated) ang.template turn<false>(x);
         } else {
           uint64_t g[8];
-          unpack8(v.g0, g);
-          unpack8(v.g1, g + 4);
+          const uint8_t* gs = stage + 1024 * (y + (kTensors - 1) * kGroups);
+          unpack8(*reinterpret_cast<const uint4*>(gs + 2 * c0), g);
+          unpack8(*reinterpret_cast<const uint4*>(gs + 2 * c1), g + 4);
           if (rotated) ang.template turn<true>(g);
           if constexpr (NORM) {
             uint64_t in0 = 0ull, in1 = 0ull;
@@ -290,7 +318,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_kernel(co
             for (int i = 0; i < 8; ++i) {
               x[i] = mul_f32x2(x[i], r2);
               const uint64_t gx = mul_f32x2(g[i], x[i]);
-              dw[i] = add_f32x2(dw[i], gx);
+              if (live) dw[i] = add_f32x2(dw[i], gx);
               if (i & 1) in1 = fma_f32x2(gx, w[i], in1);
               else in0 = fma_f32x2(gx, w[i], in0);
             }
@@ -303,12 +331,17 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_kernel(co
             for (int i = 0; i < 8; ++i) x[i] = g[i];
           }
         }
-        if ((int)(step * kGroups + y) * kHeads + head_of < heads) {
+        if (live) {
           *reinterpret_cast<uint4*>(at + y * kHeads * D + c0) = pack8(x);
           *reinterpret_cast<uint4*>(at + y * kHeads * D + c1) = pack8(x + 4);
         }
       }
     }
+  }
+  if (lane == 0 && *abort) {  // a wait gave up: the copies in flight end before the CTA's memory is given up
+    int no_abort = 0;
+    for (uint32_t i = a_count > kStages ? a_count - kStages : 0; i < a_count; ++i)
+      mbar_wait(&loaded[warp][i % kStages], (i / kStages) & 1, &no_abort, p.status, kSiteRopeDrain);
   }
   if constexpr (BWD && NORM) {
     // heads of the warp, then warps of the CTA, in a fixed order; one row of partial sums per CTA
@@ -356,9 +389,14 @@ __global__ void __launch_bounds__(256) rope_weight_grad_kernel(const float* part
 // With tokens enough to fill the GPU, the queries' and the keys' warps are in proportion to their steps
 // and a token's steps of one kind stay in one warp (its angles are computed once); with few tokens they
 // are spread over more warps, down to one step each. Returns the number of CTAs.
-int split_rope(RopeParams& p, int64_t T, int sm_count) {
+template <bool BWD, bool NORM>
+int plan_rope(RopeParams& p, int64_t T, int Hq, int Hkv, int d, int sm_count) {
+  using Tune = RopeTune<BWD, NORM>;
+  const int per_step = 32 / (d / 16) * Tune::kGroups;
+  p.steps[0] = (Hq + per_step - 1) / per_step;
+  p.steps[1] = (Hkv + per_step - 1) / per_step;
   const int total = p.steps[0] + p.steps[1];
-  const int64_t most = (int64_t)sm_count * kRopeBlocksPerSm * kRopeWarps;
+  const int64_t most = (int64_t)sm_count * Tune::kBlocks * kRopeWarps;
   const int64_t per_token = T > 0 ? most / T : 1;  // warps there are for each token
   int64_t want[2];
   for (int x = 0; x < 2; ++x) {
@@ -374,27 +412,37 @@ int split_rope(RopeParams& p, int64_t T, int sm_count) {
     want[1] = want[1] < most - queries ? want[1] : most - queries;
     want[0] = want[0] < most - want[1] ? want[0] : most - want[1];
   }
-  p.warps[0] = (int)want[0];
-  p.warps[1] = (int)want[1];
-  return (int)((want[0] + want[1] + kRopeWarps - 1) / kRopeWarps);
-}
-
-void set_steps(RopeParams& p, int Hq, int Hkv, int d, bool bwd) {
-  const int per_step = 32 / (d / 16) * (bwd ? kRopeGroups<true> : kRopeGroups<false>);
-  p.steps[0] = (Hq + per_step - 1) / per_step;
-  p.steps[1] = (Hkv + per_step - 1) / per_step;
-}
-
-template <int D, bool BWD>
-cudaError_t launch_rope(const RopeParams& p, int blocks, bool norm, bool interleaved, cudaStream_t stream) {
-  if (norm) {
-    if (interleaved) rope_kernel<D, BWD, true, true><<<blocks, kRopeThreads, 0, stream>>>(p);
-    else rope_kernel<D, BWD, true, false><<<blocks, kRopeThreads, 0, stream>>>(p);
-  } else {
-    if (interleaved) rope_kernel<D, BWD, false, true><<<blocks, kRopeThreads, 0, stream>>>(p);
-    else rope_kernel<D, BWD, false, false><<<blocks, kRopeThreads, 0, stream>>>(p);
+  // as many units for every warp: with fewer for some, the GPU would drain while the others finish
+  for (int x = 0; x < 2; ++x) {
+    const int64_t units = T * p.parts[x], rounds = want[x] > 0 ? (units + want[x] - 1) / want[x] : 1;
+    p.warps[x] = (int)((units + rounds - 1) / rounds);
   }
+  return (p.warps[0] + p.warps[1] + kRopeWarps - 1) / kRopeWarps;
+}
+
+template <int D, bool BWD, bool NORM, bool INTERLEAVED>
+cudaError_t launch_rope(const RopeParams& p, int blocks, cudaStream_t stream) {
+  auto kern = rope_kernel<D, BWD, NORM, INTERLEAVED>;
+  static std::atomic<unsigned> configured_mask{0u};  // one bit per device ordinal below 32
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 32 || !(configured_mask.load(std::memory_order_acquire) & (1u << dev))) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RopeTune<BWD, NORM>::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 32) configured_mask.fetch_or(1u << dev, std::memory_order_release);
+  }
+  kern<<<blocks, kRopeThreads, RopeTune<BWD, NORM>::kSmemBytes, stream>>>(p);
   return cudaGetLastError();
+}
+
+template <bool BWD, bool NORM>
+cudaError_t launch_rope(const RopeParams& p, int blocks, int d, int interleaved, cudaStream_t stream) {
+  if (d == 128)
+    return interleaved ? launch_rope<128, BWD, NORM, true>(p, blocks, stream)
+                       : launch_rope<128, BWD, NORM, false>(p, blocks, stream);
+  return interleaved ? launch_rope<64, BWD, NORM, true>(p, blocks, stream)
+                     : launch_rope<64, BWD, NORM, false>(p, blocks, stream);
 }
 
 cudaError_t launch_weight_grad(const float* partial, int rows, int d, float* dq_weight, float* dk_weight,
@@ -517,12 +565,12 @@ extern "C" fa_status fa_qk_norm_rope(const void* q, int64_t q_stride, const void
   int sm_count = 0;
   const int rc = fa::current_device_info(&status, &sm_count);
   if (rc != FA_OK) return (fa_status)rc;
+  p.status = status;
   if (T == 0) return FA_OK;
-  fa::set_steps(p, Hq, Hkv, d, false);
-  const int blocks = fa::split_rope(p, T, sm_count);
-  const bool norm = q_weight != nullptr;
-  const cudaError_t e = d == 128 ? fa::launch_rope<128, false>(p, blocks, norm, interleaved != 0, stream)
-                                 : fa::launch_rope<64, false>(p, blocks, norm, interleaved != 0, stream);
+  const int blocks = q_weight ? fa::plan_rope<false, true>(p, T, Hq, Hkv, d, sm_count)
+                              : fa::plan_rope<false, false>(p, T, Hq, Hkv, d, sm_count);
+  const cudaError_t e = q_weight ? fa::launch_rope<false, true>(p, blocks, d, interleaved, stream)
+                                 : fa::launch_rope<false, false>(p, blocks, d, interleaved, stream);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -534,8 +582,7 @@ extern "C" size_t fa_qk_norm_rope_bwd_workspace_bytes(int64_t T, int Hq, int Hkv
   if (sm_count <= 0) sm_count = 152;
   if ((int64_t)Hq + Hkv > (1 << 20)) return 0;
   fa::RopeParams p;
-  fa::set_steps(p, Hq, Hkv, d, true);
-  return (size_t)fa::split_rope(p, T, sm_count) * 2 * d * sizeof(float);
+  return (size_t)fa::plan_rope<true, true>(p, T, Hq, Hkv, d, sm_count) * 2 * d * sizeof(float);
 }
 
 extern "C" fa_status fa_qk_norm_rope_bwd(const void* dq_out, int64_t dq_out_stride, const void* dk_out,
@@ -574,15 +621,16 @@ extern "C" fa_status fa_qk_norm_rope_bwd(const void* dq_out, int64_t dq_out_stri
   int sm_count = 0;
   const int rc = fa::current_device_info(&status, &sm_count);
   if (rc != FA_OK) return (fa_status)rc;
-  fa::set_steps(p, Hq, Hkv, d, true);
-  const int blocks = fa::split_rope(p, T, sm_count);
+  p.status = status;
+  const int blocks = norm ? fa::plan_rope<true, true>(p, T, Hq, Hkv, d, sm_count)
+                          : fa::plan_rope<true, false>(p, T, Hq, Hkv, d, sm_count);
   const size_t need = norm ? (size_t)blocks * 2 * d * sizeof(float) : 0;
   if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_WORKSPACE;
   if (need > 0 && !fa::is_aligned(workspace, 256)) return FA_ERR_ALIGNMENT;
   p.partial = static_cast<float*>(workspace);
   if (T > 0) {
-    const cudaError_t e = d == 128 ? fa::launch_rope<128, true>(p, blocks, norm, interleaved != 0, stream)
-                                   : fa::launch_rope<64, true>(p, blocks, norm, interleaved != 0, stream);
+    const cudaError_t e = norm ? fa::launch_rope<true, true>(p, blocks, d, interleaved, stream)
+                               : fa::launch_rope<true, false>(p, blocks, d, interleaved, stream);
     if (e != cudaSuccess) return FA_ERR_CUDA;
   }
   if (!norm) return FA_OK;
