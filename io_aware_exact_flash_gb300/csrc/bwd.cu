@@ -768,9 +768,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) bwd_kernel(const __grid_consta
 
 // Row statistics: -LSE in base 2 and -delta, laid out by query tile so that a key unit fetches a
 // tile's 256 values with one bulk copy. Rows past S get -inf and 0: their P and dS are then 0. A
-// row whose LSE is -inf (no key) gets the same. One warp takes 32 consecutive rows of one head;
-// warps with consecutive numbers take consecutive heads, so the rows they read are adjacent.
+// row whose LSE is -inf (no key) gets the same. One warp takes 8 (d = 128) or 16 consecutive rows of one
+// head with every load in flight at once; warps with consecutive numbers take consecutive heads, so the
+// rows they read are adjacent.
 constexpr int kStatThreads = 256;
+constexpr int kStatUnroll = 4;  // passes of 32 lanes, 16 bytes each, over the warp's rows
+template <int D>
+constexpr int kStatRows = kStatUnroll * 256 / D;
 
 template <int D>
 __global__ void __launch_bounds__(kStatThreads) bwd_stat_kernel(StatParams p) {
@@ -781,41 +785,38 @@ __global__ void __launch_bounds__(kStatThreads) bwd_stat_kernel(StatParams p) {
   const int64_t item = (int64_t)blockIdx.x * (kStatThreads / 32) + (threadIdx.x >> 5);
   const int h = (int)(item % p.Hq);
   const int64_t rest = item / p.Hq;
-  const int blocks = p.T * (kTile / 32);
-  const int b = (int)(rest / blocks), s0 = (int)(rest % blocks) * 32;
+  const int blocks = p.T * (kTile / kStatRows<D>);
+  const int b = (int)(rest / blocks), s0 = (int)(rest % blocks) * kStatRows<D>;
   if (b >= p.B) return;
   const int sub = lane / kLanes, part = lane % kLanes;
   float mine = 0.f;  // delta of row s0 + lane
-  constexpr int kUnroll = 4;
-#pragma unroll 1
-  for (int r0 = 0; r0 < 32; r0 += kRows * kUnroll) {
-    uint4 a[kUnroll], c[kUnroll];
+  uint4 a[kStatUnroll], c[kStatUnroll];
 #pragma unroll
-    for (int x = 0; x < kUnroll; ++x) {
-      const int s = s0 + r0 + x * kRows + sub;
-      a[x] = c[x] = make_uint4(0, 0, 0, 0);
-      if (s < p.S) {
-        const int64_t off = (((int64_t)b * p.S + s) * p.Hq + h) * D + part * 8;
-        a[x] = __ldg(reinterpret_cast<const uint4*>(p.o + off));
-        c[x] = __ldg(reinterpret_cast<const uint4*>(p.dout + off));
-      }
-    }
-#pragma unroll
-    for (int x = 0; x < kUnroll; ++x) {
-      const uint32_t av[4] = {a[x].x, a[x].y, a[x].z, a[x].w}, cv[4] = {c[x].x, c[x].y, c[x].z, c[x].w};
-      float sum = 0.f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        sum = fmaf(__uint_as_float(av[k] << 16), __uint_as_float(cv[k] << 16), sum);
-        sum = fmaf(__uint_as_float(av[k] & 0xffff0000u), __uint_as_float(cv[k] & 0xffff0000u), sum);
-      }
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      // row r0 + x * kRows + k of the block sits in lanes [k * kLanes, (k + 1) * kLanes)
-      const float got = __shfl_sync(0xffffffffu, sum, (lane % kRows) * kLanes);
-      if (lane / kRows == r0 / kRows + x) mine = got;
+  for (int x = 0; x < kStatUnroll; ++x) {
+    const int s = s0 + x * kRows + sub;
+    a[x] = c[x] = make_uint4(0, 0, 0, 0);
+    if (s < p.S) {
+      const int64_t off = (((int64_t)b * p.S + s) * p.Hq + h) * D + part * 8;
+      a[x] = __ldg(reinterpret_cast<const uint4*>(p.o + off));
+      c[x] = __ldg(reinterpret_cast<const uint4*>(p.dout + off));
     }
   }
+#pragma unroll
+  for (int x = 0; x < kStatUnroll; ++x) {
+    const uint32_t av[4] = {a[x].x, a[x].y, a[x].z, a[x].w}, cv[4] = {c[x].x, c[x].y, c[x].z, c[x].w};
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      sum = fmaf(__uint_as_float(av[k] << 16), __uint_as_float(cv[k] << 16), sum);
+      sum = fmaf(__uint_as_float(av[k] & 0xffff0000u), __uint_as_float(cv[k] & 0xffff0000u), sum);
+    }
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    // row x * kRows + k of the block sits in lanes [k * kLanes, (k + 1) * kLanes)
+    const float got = __shfl_sync(0xffffffffu, sum, (lane % kRows) * kLanes);
+    if (lane / kRows == x) mine = got;
+  }
+  if (lane >= kStatRows<D>) return;
   const int s = s0 + lane;
   float nlse = -INFINITY, ndelta = 0.f;
   if (s < p.S) {
@@ -852,7 +853,7 @@ cudaError_t launch_bwd(const StatParams& sp, const BwdParams& p, int64_t units, 
     if (e != cudaSuccess) return e;
     if (dev < 32) configured_mask.fetch_or(1u << dev, std::memory_order_release);
   }
-  const int64_t items = (int64_t)p.B * p.Hq * p.T * (kTile / 32);
+  const int64_t items = (int64_t)p.B * p.Hq * p.T * (kTile / kStatRows<D>);
   const int64_t blocks = (items + kStatThreads / 32 - 1) / (kStatThreads / 32);
   bwd_stat_kernel<D><<<(unsigned)blocks, kStatThreads, 0, stream>>>(sp);
   cudaError_t e = cudaGetLastError();
@@ -878,7 +879,7 @@ bool bwd_sizes_ok(int B, int Hq, int Hkv, int S) { return B > 0 && Hq > 0 && Hkv
 
 bool bwd_too_large(int B, int Hq, int Hkv, int S, int d) {
   return (long long)B * S > (1LL << 31) - 1 || (long long)B * S * Hq > (1LL << 40) / d ||
-         (long long)B * (Hq + (long long)Hkv) > ((1LL << 31) - 1) / (4 * bwd_tiles(S));
+         (long long)B * (Hq + (long long)Hkv) > ((1LL << 31) - 1) / (16 * bwd_tiles(S));
 }
 
 }  // namespace
