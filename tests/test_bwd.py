@@ -114,3 +114,204 @@ def test_bwd_matches_fp64(B, S, Hq, Hkv, d, causal, with_dlse):
     grads = fa.fa_bwd(q, k, v, o, lse, do, causal=causal, scale=scale, dlse=dlse)
     assert fa.fa_get_device_status() == (0, 0)
     check(grads, q, k, v, o, lse, do, dlse, causal, scale, f"bwd {B, S, Hq, Hkv, d, causal}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,causal", [(64, False), (128, True)])
+def test_bwd_long_rows(d, causal):
+    """Many tiles per unit (the rings and barrier phases wrap many times), an odd length."""
+    import io_aware_exact_flash_gb300 as fa
+
+    q, k, v, do, _ = inputs(1, 2501, 2, 1, d)
+    scale = 1.0 / math.sqrt(d)
+    o, lse = fa.fa_fwd(q, k, v, causal=causal, scale=scale)
+    grads = fa.fa_bwd(q, k, v, o, lse, do, causal=causal, scale=scale)
+    check(grads, q, k, v, o, lse, do, None, causal, scale, "long rows")
+
+
+@pytest.mark.gpu
+def test_bwd_matches_differences():
+    """<gradient, direction> against central differences of the forward pass in fp64. Each gradient is
+    within 2 u of the formula's (asserted above); o is given to the backward rounded to bf16, which moves
+    delta, and so each gradient, by at most another u of its terms: 4 u of the norms bounds both."""
+    import io_aware_exact_flash_gb300 as fa
+
+    B, S, Hq, Hkv, d = 1, 200, 4, 2, 64
+    q, k, v, do, dlse = inputs(B, S, Hq, Hkv, d, seed=5)
+    scale = 1.0 / math.sqrt(d)
+    o, lse = fa.fa_fwd(q, k, v, causal=True, scale=scale)
+    grads = fa.fa_bwd(q, k, v, o, lse, do, causal=True, scale=scale, dlse=dlse)
+
+    def loss(q, k, v):
+        s = torch.einsum("bihd,bjhd->bhij", q, k.repeat_interleave(Hq // Hkv, 2)) * scale
+        s = s.masked_fill(torch.ones(S, S, dtype=torch.bool, device=q.device).triu(1), float("-inf"))
+        out = torch.einsum("bhij,bjhd->bihd", s.softmax(-1), v.repeat_interleave(Hq // Hkv, 2))
+        return (out * do.double()).sum() + (s.logsumexp(-1).permute(0, 2, 1) * dlse.double()).sum()
+
+    x = [t.double() for t in (q, k, v)]
+    g = torch.Generator(device="cuda").manual_seed(9)
+    for i in range(3):
+        grad = grads[i].double()
+        way = grad / grad.norm() + torch.randn(grad.shape, generator=g, device="cuda").double() / grad.numel() ** 0.5
+        eps = 1e-4
+        up, down = list(x), list(x)
+        up[i], down[i] = x[i] + eps * way, x[i] - eps * way
+        fd = float((loss(*up) - loss(*down)) / (2 * eps))
+        assert abs(float((grad * way).sum()) - fd) <= 4 * U * float(grad.norm() * way.norm())
+
+
+@pytest.mark.gpu
+def test_bwd_large_scores():
+    """Sharp softmax rows (scores of tens): most P are 0, LSE and scores cancel. The exponent's fp32 error
+    is at most 2^-24 (|s| + |LSE|) log2(e) 4 < 2^-13 for magnitudes below 300: inside the bound's 2^-10."""
+    import io_aware_exact_flash_gb300 as fa
+
+    q, k, v, do, _ = inputs(1, 300, 2, 2, 64, gain=4.0)
+    o, lse = fa.fa_fwd(q, k, v, causal=True)
+    assert float(lse.abs().max()) < 300
+    grads = fa.fa_bwd(q, k, v, o, lse, do, causal=True)
+    check(grads, q, k, v, o, lse, do, None, True, 1 / 8.0, "large scores")
+
+
+@pytest.mark.gpu
+def test_bwd_rows_without_keys_and_far_lse():
+    """LSE = -inf marks a row without keys: no gradient from it or to it. Checked against the formulas."""
+    import io_aware_exact_flash_gb300 as fa
+
+    q, k, v, do, dlse = inputs(2, 150, 2, 1, 128)
+    o, lse = fa.fa_fwd(q, k, v, causal=False)
+    lse[0, 7, 0] = lse[1, 149, 1] = lse[0, 64, 1] = float("-inf")
+    grads = fa.fa_bwd(q, k, v, o, lse, do, causal=False, dlse=dlse)
+    assert not grads[0][0, 7, 0].any() and not grads[0][1, 149, 1].any()
+    dl = dlse.masked_fill(torch.isneginf(lse), 0.0)
+    check(grads, q, k, v, o, lse, do, dl, False, 1 / math.sqrt(128), "rows without keys")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_bwd_non_finite_stays_in_its_head(d):
+    """A NaN reaches gradients of its own batch entry and kv head only; a masked dO of infinity does not
+    reach the keys of other tiles."""
+    import io_aware_exact_flash_gb300 as fa
+
+    q, k, v, do, _ = inputs(2, 260, 4, 2, d)
+    o, lse = fa.fa_fwd(q, k, v, causal=True)
+    clean = fa.fa_bwd(q, k, v, o, lse, do, causal=True)
+    bad = do.clone()
+    bad[1, 3, 2, 5] = float("nan")   # kv head 1 of batch entry 1
+    grads = fa.fa_bwd(q, k, v, o, lse, bad, causal=True)
+    for got, ref, heads in zip(grads, clean, (slice(2, 4), slice(1, 2), slice(1, 2))):
+        keep = torch.ones(got.shape[:3], dtype=torch.bool, device="cuda")
+        keep[1, :, heads] = False
+        assert torch.equal(got[keep], ref[keep])
+    assert torch.isnan(grads[0][1, 3, 2]).any()
+    # row 3 is in the first tile: keys of later tiles never see it
+    assert torch.equal(grads[1][1, 128:], clean[1][1, 128:]) and torch.equal(grads[2][1, 128:], clean[2][1, 128:])
+
+
+@pytest.mark.gpu
+def test_bwd_is_deterministic_and_leaves_the_rest_alone():
+    import io_aware_exact_flash_gb300 as fa
+
+    q, k, v, do, _ = inputs(2, 333, 6, 3, 128)
+    keep = [t.clone() for t in (q, k, v, do)]
+    o, lse = fa.fa_fwd(q, k, v, causal=True)
+    first = fa.fa_bwd(q, k, v, o, lse, do, causal=True)
+    # outputs inside larger buffers, 16-byte but not 32-byte aligned, with sentinels around them
+    outs, bufs = [], []
+    for t in (q, k, v):
+        buf = torch.full((t.numel() + 64,), 7.0, device="cuda", dtype=torch.bfloat16)
+        outs.append(buf[8:8 + t.numel()].view(t.shape))
+        bufs.append(buf)
+    need = fa.fa_bwd_workspace_bytes(2, 6, 3, 333, 128, True)
+    ws = torch.full((need + 512,), 255, device="cuda", dtype=torch.uint8)  # garbage (NaN) inside
+    off = -ws.data_ptr() % 256
+    again = fa.fa_bwd(q, k, v, o, lse, do, causal=True, dq=outs[0], dk=outs[1], dv=outs[2],
+                      workspace=ws[off:off + need])
+    for a, b, out, buf in zip(first, again, outs, bufs):
+        assert b is out and torch.equal(a, b)
+        assert (buf[:8] == 7).all() and (buf[8 + out.numel():] == 7).all()
+    assert (ws[off + need:] == 255).all()
+    assert all(torch.equal(a, b) for a, b in zip(keep, (q, k, v, do)))
+
+
+@pytest.mark.gpu
+def test_bwd_in_graphs_that_share_a_workspace():
+    """Two captured backward passes of different shapes, one workspace, replayed in turn with new inputs."""
+    import io_aware_exact_flash_gb300 as fa
+
+    shapes = [(1, 200, 4, 2, 64, True), (2, 130, 2, 2, 128, False)]
+    need = max(fa.fa_bwd_workspace_bytes(B, Hq, Hkv, S, d, c) for B, S, Hq, Hkv, d, c in shapes)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    graphs, states = [], []
+    for B, S, Hq, Hkv, d, c in shapes:
+        q, k, v, do, _ = inputs(B, S, Hq, Hkv, d)
+        o, lse = fa.fa_fwd(q, k, v, causal=c)
+        out = tuple(torch.zeros_like(t) for t in (q, k, v))
+        st = (q, k, v, o, lse, do)
+        run = lambda st=st, c=c, out=out: fa.fa_bwd(*st, causal=c, dq=out[0], dk=out[1], dv=out[2], workspace=ws)  # noqa: E731
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            run()
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        graphs.append(graph)
+        states.append((st, out, c))
+    for turn in range(2):
+        for graph, (st, out, c) in zip(graphs, states):
+            st[5].copy_(torch.randn_like(st[5].float()).bfloat16())  # another dO
+            for t in out:
+                t.zero_()
+            graph.replay()
+        for st, out, c in states:
+            want = fa.fa_bwd(*st, causal=c)
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.gpu
+def test_bwd_on_two_streams_at_once():
+    import io_aware_exact_flash_gb300 as fa
+
+    cases = [inputs(1, 700, 8, 4, 128, seed=s)[:4] for s in (1, 2)]
+    fwd = [fa.fa_fwd(q, k, v, causal=True) for q, k, v, _ in cases]
+    want = [fa.fa_bwd(q, k, v, o, l, do, causal=True) for (q, k, v, do), (o, l) in zip(cases, fwd)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            (q, k, v, do), (o, l) = cases[i], fwd[i]
+            got[i].append(fa.fa_bwd(q, k, v, o, l, do, causal=True, stream=s))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
+
+
+@pytest.mark.gpu
+def test_bwd_python_refusals():
+    import io_aware_exact_flash_gb300 as fa
+
+    q, k, v, do, dlse = inputs(1, 64, 2, 2, 64)
+    o, lse = fa.fa_fwd(q, k, v)
+    good = dict(q=q, k=k, v=v, out=o, lse=lse, dout=do)
+    for kw in (dict(q=q.half()), dict(dout=do.cpu())):
+        with pytest.raises(TypeError):
+            fa.fa_bwd(**{**good, **kw})
+    wide = torch.cat([do, do], 3)
+    for kw in (dict(dout=wide[..., :64]), dict(out=o[:, :32].contiguous()), dict(lse=lse.double()),
+               dict(lse=lse[..., :1].contiguous()), dict(k=k[:, :, :1].contiguous()), dict(dlse=dlse[:, :3]),
+               dict(dq=torch.empty_like(q)[:, :32]), dict(dk=torch.empty_like(k).float()),
+               dict(workspace=torch.empty(4096, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            fa.fa_bwd(**{**good, **kw})
+    with pytest.raises(fa.FaError) as e:
+        fa.fa_bwd(**good, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    assert e.value.code == 4  # FA_ERR_WORKSPACE
+    for kw in (dict(dq=q), dict(dk=v), dict(dv=torch.empty_like(v), dk=None, dq=do)):  # outputs over inputs
+        with pytest.raises(fa.FaError) as e:
+            fa.fa_bwd(**{**good, **kw})
+        assert e.value.code == 1
