@@ -56,6 +56,7 @@ enum : uint32_t {
   kSiteBwdTurn = 41,
   kSiteBwdTake = 42,
   kSiteBwdAccFree = 43,
+  kSiteBwdResFree = 44,
 };
 
 struct alignas(64) BwdParams {
@@ -104,7 +105,7 @@ struct Ctl {
   uint4 resp[2];                           // launch cancellation responses
   uint64_t resp_full[2], resp_empty[2];
   StepBars<D> kind[2];                     // query units, key units
-  uint64_t resident, acc, acc_free;        // one phase per unit
+  uint64_t resident[2], res_free[2], acc, acc_free;  // one phase per unit
   uint32_t tmem;
   int abort;
 };
@@ -257,7 +258,7 @@ __device__ __forceinline__ int taken_unit(const BwdParams& p, Ctl<D>& ctl, int r
 // The last copy issued into each slot (bit 16 kind + slot), statistics buffer (after the slots),
 // the resident tiles and the two response slots, with its barrier's phase.
 struct Copies {
-  static constexpr int kResident = 12, kResponse = 13;
+  static constexpr int kResident = 12, kResponse = 14;
   uint32_t issued = 0, parity = 0;
   __device__ __forceinline__ void note(int bit, int phase) {
     issued |= 1u << bit;
@@ -265,8 +266,7 @@ struct Copies {
   }
 };
 
-// TMA producer (lane 0 of its warp): the streamed tiles and, once the previous unit's products are
-// done, the resident ones. Key unit: dO_i, Q_i and the tile's statistics; query unit: K_j and V_j.
+// TMA producer (lane 0 of its warp): the streamed tiles and the resident ones. Key unit: dO_i, Q_i and the tile's statistics; query unit: K_j and V_j.
 // r: units this CTA has run before; first: steps it has run in units of this kind; same: the previous
 // unit was of this kind too (its slots are then released one by one).
 template <int D, bool KEY>
@@ -306,12 +306,15 @@ __device__ __forceinline__ void produce(const BwdParams& p, const BwdUnit& u, ui
       copies.note(16 + C::kSlots + s, x >> 1);
     }
     if (i == 0) {
-      if (r > 0 && same) step_wait(&ctl.acc, (r - 1) & 1, abort, kSiteBwdAcc);
-      if (*abort) return;
-      mbar_arrive_expect_tx(&ctl.resident, 2 * TB);
-      copies.note(Copies::kResident, r);
-      load_tile<D>(smem, KEY ? &p.tm_k : &p.tm_q, &ctl.resident, u.h, u.tile * kTile, u.b, policy);
-      load_tile<D>(smem + TB, KEY ? &p.tm_v : &p.tm_do, &ctl.resident, u.h, u.tile * kTile, u.b, policy);
+      // each resident tile as soon as the previous unit's last product that reads it is done
+      for (int x = 0; x < 2; ++x) {
+        if (r > 0) step_wait(&ctl.res_free[x], (r - 1) & 1, abort, kSiteBwdResFree);
+        if (*abort) return;
+        mbar_arrive_expect_tx(&ctl.resident[x], TB);
+        copies.note(Copies::kResident + x, r);
+        load_tile<D>(smem + x * TB, KEY ? (x ? &p.tm_v : &p.tm_k) : (x ? &p.tm_do : &p.tm_q), &ctl.resident[x], u.h,
+                     u.tile * kTile, u.b, policy);
+      }
     }
     if (++t == u.first + u.per) {
       t = u.first;
@@ -331,9 +334,9 @@ __device__ __forceinline__ void drain_copies(const BwdParams& p, Ctl<D>& ctl, co
     if (!(copies.issued & (1u << bit))) continue;
     StepBars<D>& bars = ctl.kind[bit >> 4];
     const int s = bit & 15;
-    uint64_t* bar = bit == Copies::kResident ? &ctl.resident
-                    : bit == Copies::kResponse || bit == Copies::kResponse + 1 ? &ctl.resp_full[bit - Copies::kResponse]
-                    : s < NS ? &bars.full[s] : &bars.stat_full[s - NS];
+    uint64_t* bar = bit < Copies::kResident || bit > 15 ? (s < NS ? &bars.full[s] : &bars.stat_full[s - NS])
+                    : bit < Copies::kResponse           ? &ctl.resident[bit - Copies::kResident]
+                                                        : &ctl.resp_full[bit - Copies::kResponse];
     step_wait(bar, (copies.parity >> bit) & 1, &no_abort, kSiteBwdDrain);
   }
 }
@@ -379,6 +382,7 @@ __device__ __forceinline__ void issue_mmas(const BwdParams& p, int n, uint8_t* s
   };
   // A slot is released by the products that read it: in a key unit one of each chain.
   // scores: S^T = K Q_i^T, S = Q K_j^T; dprob: dP^T = V dO_i^T, dP = dO V_j^T
+  // The unit's last one releases the chain's resident tile.
   auto tile_product = [&](int x, int which, uint32_t col, uint64_t* ready, bool release) {
     const int slot = L::slot_of(x, which).slot;
     wait_full(x, which);
@@ -388,6 +392,7 @@ __device__ __forceinline__ void issue_mmas(const BwdParams& p, int n, uint8_t* s
       mma_scores<D>(tmem + col, a, bk + (uint64_t)(slot * (TB >> 4)));
       mma_commit(ready);
       if (release) mma_commit(&bars.empty[slot]);
+      if (x == first + n - 1) mma_commit(&ctl.res_free[CHAIN]);
     }
     __syncwarp();
   };
@@ -404,7 +409,7 @@ __device__ __forceinline__ void issue_mmas(const BwdParams& p, int n, uint8_t* s
     }
     __syncwarp();
   };
-  step_wait(&ctl.resident, r & 1, abort, kSiteBwdResident);
+  step_wait(&ctl.resident[CHAIN], r & 1, abort, kSiteBwdResident);
   if (!same) wait_acc_free();  // the kinds place their accumulators and scores differently
   if constexpr (CHAIN == 0) {
     scores(first);
@@ -648,14 +653,39 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
   tc_fence_before();
   __syncwarp();
   if (lane == 0) mbar_arrive(&ctl.acc_free);
-  if (srow < p.S) {
-    if ((reinterpret_cast<uintptr_t>(base) & 31) == 0) {  // whole 32-byte sectors
+  // Rows of four lanes are exchanged so that each of the four stores 32 bytes of the same row: 128 bytes in
+  // a row per store (32 at d = 64, query unit: two lanes, 64 bytes).
+  constexpr int kUnits = kCols / 16;               // 32-byte units of this lane's row
+  constexpr int kGroup = kUnits < 4 ? kUnits : 4;  // lanes that exchange
 #pragma unroll
-      for (int k = 0; k < kCols / 16; ++k) st_global_32(base + 16 * k, w + 8 * k);
-    } else {
+  for (int x = 1; x < kGroup; x *= 2) {
+    const bool upper = lane & x;
 #pragma unroll
-      for (int k = 0; k < kCols / 8; ++k)
-        *reinterpret_cast<uint4*>(base + 8 * k) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    for (int k = 0; k < kUnits; ++k) {
+      if (k & x) continue;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        uint32_t &lo = w[8 * k + c], &hi = w[8 * (k + x) + c];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? lo : hi, x);
+        if (upper) lo = got;
+        else hi = got;
+      }
+    }
+  }
+  // unit k of lane l is now unit (k / kGroup) kGroup + l % kGroup of row k % kGroup of its group
+  const int own = lane % kGroup;
+  __nv_bfloat16* rows = base - (int64_t)own * heads * D + 16 * own;
+  const bool wide = (reinterpret_cast<uintptr_t>(base) & 31) == 0;  // (the same for every row)
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k) {
+    __nv_bfloat16* dst = rows + (int64_t)(k % kGroup) * heads * D + 16 * (k / kGroup) * kGroup;
+    if (srow - own + k % kGroup < p.S) {
+      if (wide) {
+        st_global_32(dst, w + 8 * k);
+      } else {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(w[8 * k], w[8 * k + 1], w[8 * k + 2], w[8 * k + 3]);
+        *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[8 * k + 4], w[8 * k + 5], w[8 * k + 6], w[8 * k + 7]);
+      }
     }
   }
 }
@@ -718,7 +748,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) bwd_kernel(const __grid_consta
       mbar_init(&ctl.resp_full[s], 1);
       mbar_init(&ctl.resp_empty[s], kBwdWalkers);
     }
-    mbar_init(&ctl.resident, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctl.resident[s], 1);
+      mbar_init(&ctl.res_free[s], 1);
+    }
     mbar_init(&ctl.acc, 2);
     mbar_init(&ctl.acc_free, 8);
     fence_mbar_init();
