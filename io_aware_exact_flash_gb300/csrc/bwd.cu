@@ -279,7 +279,16 @@ __device__ __forceinline__ void produce(const BwdParams& p, const BwdUnit& u, ui
   volatile int* abort = &ctl.abort;
   const uint64_t policy = policy_evict_last();  // every tile is read by many units
   uint8_t* slots = smem + 2 * TB;
-  if (r > 0 && !same) step_wait(&ctl.acc, (r - 1) & 1, abort, kSiteBwdAcc);
+  if (r > 0 && !same) {
+    // The ring's memory belongs to the other kind's slots until each has been released. (Not a wait for
+    // the previous unit's accumulators: this warp can be two units ahead of those, and a wait by parity
+    // then passes at once.)
+    for (int s = 0; s < C::kSlots; ++s) {
+      const int bit = 16 * !KEY + s;
+      if (copies.issued >> bit & 1)
+        step_wait(&ctl.kind[!KEY].empty[s], copies.parity >> bit & 1, abort, kSiteBwdEmpty);
+    }
+  }
   int t = u.first, h = KEY ? u.h * p.group : u.h / p.group;
   for (int i = 0; i < u.steps; ++i) {
 #pragma unroll

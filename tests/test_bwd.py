@@ -117,6 +117,30 @@ def test_bwd_matches_fp64(B, S, Hq, Hkv, d, causal, with_dlse):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,S,Hq,Hkv,d,causal", [
+    (1, 384, 64, 64, 64, True),     # a CTA's second unit has one to three steps
+    (1, 384, 64, 64, 128, True),
+    (1, 100, 400, 400, 64, False),  # one step each, several units per CTA
+    (1, 100, 400, 200, 128, True),
+    (2, 130, 120, 120, 128, False), # two steps
+    (2, 300, 96, 32, 64, False),
+])
+def test_bwd_short_units_one_after_the_other(B, S, Hq, Hkv, d, causal):
+    """CTAs that run many short units of both kinds: the loads of the next units start while the last ones
+    are still computed. Every one of several runs has the same bits."""
+    import io_aware_exact_flash_gb300 as fa
+
+    q, k, v, do, _ = inputs(B, S, Hq, Hkv, d)
+    scale = 1.0 / math.sqrt(d)
+    o, lse = fa.fa_fwd(q, k, v, causal=causal, scale=scale)
+    runs = [fa.fa_bwd(q, k, v, o, lse, do, causal=causal, scale=scale) for _ in range(10)]
+    check(runs[0], q, k, v, o, lse, do, None, causal, scale, f"short units {B, S, Hq, Hkv, d, causal}")
+    for g in runs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(g, runs[0]))
+    assert fa.fa_get_device_status() == (0, 0)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("d,causal", [(64, False), (128, True)])
 def test_bwd_long_rows(d, causal):
     """Many tiles per unit (the rings and barrier phases wrap many times), an odd length."""
