@@ -59,13 +59,35 @@ enum : uint32_t {
   kSiteBwdResFree = 44,
 };
 
+// n / d for 0 <= n < 2^31 by a multiplication: with s = ceil(log2 d) and m = ceil(2^(31 + s) / d),
+// n m / 2^(31 + s) exceeds n / d by less than n / 2^31 / d, too little to reach the next integer. (A
+// unit's place in the order takes three divisions, which every warp does between two units.)
+struct Divisor {
+  uint32_t d, mul, shift;
+  void set(uint32_t value) {
+    d = value;
+    shift = 0;
+    while ((1u << shift) < d) ++shift;
+    mul = (uint32_t)(((1ull << (31 + shift)) + d - 1) / d);
+  }
+  __device__ __forceinline__ uint32_t divide(uint32_t n) const {
+    return (uint32_t)(((uint64_t)n * mul) >> (31 + shift));
+  }
+};
+
+// The order of one kind's units: chunks of `heads` heads whose units are scheduled together.
+struct UnitOrder {
+  Divisor per_chunk, width, last_width, heads_per_entry;  // units and heads per chunk; heads of a batch entry
+  uint32_t full_chunks;
+};
+
 struct alignas(64) BwdParams {
   CUtensorMap tm_q, tm_k, tm_v, tm_do;  // (d, heads, S, B), boxes of 64 x 1 x 128 x 1
   const float* stat;                    // [B, Hq, T, 2, 128]: -LSE log2(e), then -delta
   __nv_bfloat16 *dq, *dk, *dv;
   int B, S, T, Hq, Hkv, group, causal;
   int kv_units;                         // key units come first in the grid
-  int kv_chunk, q_chunk;                // heads whose units are scheduled together
+  UnitOrder order[2];                   // query units, key units
   float scale, scale_log2;
   DeviceStatus* status;
 };
@@ -124,19 +146,16 @@ struct BwdUnit {
 // come first. Key units precede query units: they are the long ones when heads share keys.
 __device__ __forceinline__ BwdUnit bwd_unit(const BwdParams& p, int index) {
   BwdUnit u;
-  int r = index;
-  u.key = r < p.kv_units;
-  if (!u.key) r -= p.kv_units;
-  const int heads = u.key ? p.Hkv : p.Hq;
-  const int chunk_heads = u.key ? p.kv_chunk : p.q_chunk;
-  const int chunk = r / (chunk_heads * p.T);
-  const int head0 = chunk * chunk_heads;
-  const int width = min(chunk_heads, p.B * heads - head0);
-  const int rc = r - chunk * chunk_heads * p.T;
-  const int rank = rc / width;
-  const int head = head0 + rc % width;
-  u.b = head / heads;
-  u.h = head % heads;
+  u.key = index < p.kv_units;
+  const UnitOrder& o = p.order[u.key];
+  const uint32_t r = u.key ? index : index - p.kv_units;
+  const uint32_t chunk = o.per_chunk.divide(r);
+  const uint32_t rc = r - chunk * o.per_chunk.d;
+  const Divisor& w = chunk < o.full_chunks ? o.width : o.last_width;
+  const int rank = (int)w.divide(rc);
+  const uint32_t head = chunk * o.width.d + (rc - rank * w.d);
+  u.b = (int)o.heads_per_entry.divide(head);
+  u.h = (int)(head - u.b * o.heads_per_entry.d);
   u.tile = (u.key || !p.causal) ? rank : p.T - 1 - rank;
   u.first = (u.key && p.causal) ? u.tile : 0;
   u.per = !p.causal ? p.T : (u.key ? p.T - u.tile : u.tile + 1);
@@ -650,13 +669,16 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
   base += (((int64_t)u.b * p.S + srow) * heads + u.h) * D;
   const float mul = (KEY && g == 0) ? 1.f : p.scale;
   uint32_t w[kCols / 2];
+  constexpr int kLoad = kCols < 64 ? 1 : 2;  // 32-column loads in flight
 #pragma unroll
-  for (int cc = 0; cc < kCols / 32; ++cc) {
-    uint32_t v[32];
-    tmem_ld32(tacc + 32 * cc, v);
-    tmem_ld_wait(v);
+  for (int cc = 0; cc < kCols / 32; cc += kLoad) {
+    uint32_t v[32 * kLoad];
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
+    for (int x = 0; x < kLoad; ++x) tmem_ld32(tacc + 32 * (cc + x), v + 32 * x);
+#pragma unroll
+    for (int x = 0; x < kLoad; ++x) tmem_ld_wait(v + 32 * x);
+#pragma unroll
+    for (int k = 0; k < 16 * kLoad; ++k)
       w[16 * cc + k] = pack_bf16x2(__uint_as_float(v[2 * k]) * mul, __uint_as_float(v[2 * k + 1]) * mul);
   }
   tc_fence_before();
@@ -1004,13 +1026,17 @@ extern "C" fa_status fa_bwd(const void* q, const void* k, const void* v, const v
   p.group = Hq / Hkv;
   p.causal = causal ? 1 : 0;
   p.kv_units = p.T * B * Hkv;
-  auto chunk = [&](int heads) {
-    int c = (sm_count + p.T / 2) / p.T;
-    if (c < 1) c = 1;
-    return c < heads ? c : heads;
-  };
-  p.kv_chunk = chunk(B * Hkv);
-  p.q_chunk = chunk(B * Hq);
+  for (int key = 0; key < 2; ++key) {
+    const int per_entry = key ? Hkv : Hq, heads = B * per_entry;
+    int width = (sm_count + p.T / 2) / p.T;
+    width = width < 1 ? 1 : width < heads ? width : heads;
+    fa::UnitOrder& order = p.order[key];
+    order.per_chunk.set((uint32_t)width * p.T);
+    order.width.set(width);
+    order.full_chunks = heads / width;
+    order.last_width.set(heads % width ? heads % width : width);
+    order.heads_per_entry.set(per_entry);
+  }
   p.scale = scale;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.status = status;
