@@ -496,21 +496,6 @@ __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t* r) 
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
 }
 
-// Overwrite this row's TMEM columns outside [lo, hi) of the 64 at taddr.
-__device__ __noinline__ void mask_columns(uint32_t taddr, int lo, int hi, uint32_t value) {
-#pragma unroll 1
-  for (int cc = 0; cc < 2; ++cc) {
-    uint32_t r[32];
-    tmem_ld32(taddr + 32 * cc, r);
-    tmem_ld_wait(r);
-#pragma unroll
-    for (int c = 0; c < 32; ++c)
-      if (32 * cc + c < lo || 32 * cc + c >= hi) r[c] = value;
-    tmem_st32(taddr + 32 * cc, r);
-  }
-  tmem_st_wait();
-}
-
 // P and dS of one row's 64 columns per step, then the gradients' epilogue.
 template <int D, bool KEY>
 __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u, uint8_t* smem, Ctl<D>& ctl, int r,
@@ -554,9 +539,8 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
     tc_fence_after();
     uint64_t pr[32];  // P: 64 values in pairs
     const uint32_t ts = tmem + L::col_s(i) + half_off;
-    // Masked tiles (few): the masked scores become -inf in TMEM, and dP there 0 below, so that the
-    // path every tile takes has no mask in it. (Not 0 times dP: it may be infinite or NaN there.)
-    if (masked) mask_columns(ts, lo, hi, 0xff800000u);
+    // Masked tiles (few): the masked scores become -inf in TMEM, so that the path every tile takes has no
+    // mask in it. P is 0 there, and so is dS (of finite dP).
     if constexpr (KEY) {
       uint32_t sr[64];
       tmem_ld_frag(ts, sr);
@@ -566,6 +550,12 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
       for (int q = 0; q < 8; ++q) nl[q] = st[4 * q];
       tmem_ld_wait(sr);
       tmem_ld_wait(sr + 32);
+      if (masked) {
+        const int first_col = (lane >> 2) + (warp & 3) * 32 - 64 * g - 2 * (lane & 3);
+#pragma unroll
+        for (int k = 0; k < 64; ++k)  // row 16 (k / 32) + 8 (k / 2 % 2) of this thread's four, column 8 (k / 4 % 8) + k % 2
+          if (8 * ((k >> 2) & 7) + (k & 1) < first_col + 16 * (k >> 5) + 8 * ((k >> 1) & 1)) sr[k] = 0xff800000u;
+      }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t pk[16];
@@ -591,6 +581,11 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
       tmem_ld32(ts + 32, sr + 32);
       tmem_ld_wait(sr);
       tmem_ld_wait(sr + 32);
+      if (masked) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          if (c >= hi) sr[c] = 0xff800000u;
+      }
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
         float x0, x1, x2, x3;
@@ -604,7 +599,6 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
     __syncwarp();
     tc_fence_after();
     const uint32_t td = tmem + L::kColDp + half_off;
-    if (masked) mask_columns(td, lo, hi, 0u);
     if constexpr (KEY) {
       uint32_t dr[64];
       tmem_ld_frag(td, dr);
