@@ -75,7 +75,7 @@ struct Divisor {
   }
 };
 
-// The order of one kind's units: chunks of `heads` heads whose units are scheduled together.
+// The order of one kind's units: chunks of `width` heads whose units are scheduled together.
 struct UnitOrder {
   Divisor per_chunk, width, last_width, heads_per_entry;  // units and heads per chunk; heads of a batch entry
   uint32_t full_chunks;
@@ -217,6 +217,11 @@ __device__ __forceinline__ bool step_wait(uint64_t* bar, uint32_t parity, volati
   return true;
 }
 
+// A wait by parity is right only while the barrier is in the awaited phase or the one after it. Every wait
+// below is of that sort: a warp waits for each phase of a barrier in turn, or for a phase that it knows cannot
+// be two away (the slots' barriers by their fill counts, acc_free because the last p or ds wait needed every
+// math warp past the unit before).
+//
 // What every role of a CTA needs to know of its unit; KEY is the kind of unit.
 template <int D, bool KEY>
 struct Layout {
@@ -285,7 +290,8 @@ struct Copies {
   }
 };
 
-// TMA producer (lane 0 of its warp): the streamed tiles and the resident ones. Key unit: dO_i, Q_i and the tile's statistics; query unit: K_j and V_j.
+// TMA producer (lane 0 of its warp): the streamed tiles and the resident ones. Key unit: dO_i, Q_i and the
+// tile's statistics; query unit: K_j and V_j.
 // r: units this CTA has run before; first: steps it has run in units of this kind; same: the previous
 // unit was of this kind too (its slots are then released one by one).
 template <int D, bool KEY>
@@ -955,7 +961,7 @@ int64_t bwd_tiles(int S) { return ((int64_t)S + kTile - 1) / kTile; }
 bool bwd_sizes_ok(int B, int Hq, int Hkv, int S) { return B > 0 && Hq > 0 && Hkv > 0 && S > 0 && Hq % Hkv == 0; }
 
 bool bwd_too_large(int B, int Hq, int Hkv, int S, int d) {
-  return (long long)B * S > (1LL << 31) - 1 || (long long)B * S * Hq > (1LL << 40) / d ||
+  return S > (1 << 30) || (long long)B * S > (1LL << 31) - 1 || (long long)B * S * Hq > (1LL << 40) / d ||
          (long long)B * (Hq + (long long)Hkv) > ((1LL << 31) - 1) / (16 * bwd_tiles(S));
 }
 

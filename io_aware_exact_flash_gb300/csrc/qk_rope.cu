@@ -531,6 +531,11 @@ fa_status check_rows(const Rows& r, int64_t T, int d) {
   return FA_OK;
 }
 
+// Whether a plain range of memory shares a byte with the rows' span (rows and what lies between them).
+bool in_rows(const void* ptr, uint64_t bytes, const Rows& r, int64_t T, int d) {
+  return T > 0 && r.ptr && overlaps(ptr, bytes, r.ptr, (uint64_t)(T - 1) * r.stride * 2 + (uint64_t)r.heads * d * 2);
+}
+
 // An output may be one of the inputs itself (same pointer and stride: each element is read before it
 // is written, by the same thread); otherwise the two share nothing.
 bool bad_output(const Rows& out, const Rows& in, int64_t T, int d) {
@@ -561,6 +566,11 @@ extern "C" fa_status fa_qk_norm_rope(const void* q, int64_t q_stride, const void
     p.out_stride[x] = out[x].stride;
   }
   if (fa::rows_overlap(out[0], out[1], T, d)) return FA_ERR_INVALID_ARG;
+  for (const fa::Rows& o : out)
+    if (fa::in_rows(q_weight, 2 * d, o, T, d) || fa::in_rows(k_weight, 2 * d, o, T, d) ||
+        (rot_dim > 0 && (fa::in_rows(positions, (uint64_t)num_axes * T * 4, o, T, d) ||
+                         fa::in_rows(inv_freq, 2 * rot_dim, o, T, d))))
+      return FA_ERR_INVALID_ARG;
   fa::DeviceStatus* status = nullptr;
   int sm_count = 0;
   const int rc = fa::current_device_info(&status, &sm_count);
@@ -616,7 +626,28 @@ extern "C" fa_status fa_qk_norm_rope_bwd(const void* dq_out, int64_t dq_out_stri
     p.out_stride[x] = out[x].stride;
   }
   if (fa::rows_overlap(out[0], out[1], T, d)) return FA_ERR_INVALID_ARG;
+  for (const fa::Rows& o : out)
+    if (fa::in_rows(q_weight, 2 * d, o, T, d) || fa::in_rows(k_weight, 2 * d, o, T, d) ||
+        (rot_dim > 0 && (fa::in_rows(positions, (uint64_t)num_axes * T * 4, o, T, d) ||
+                         fa::in_rows(inv_freq, 2 * rot_dim, o, T, d))))
+      return FA_ERR_INVALID_ARG;
   if (!fa::is_aligned(dq_weight, 4) || !fa::is_aligned(dk_weight, 4)) return FA_ERR_ALIGNMENT;
+  if (norm) {  // the sums' outputs and the scratch lie apart from each other and from every tensor
+    const struct { const void* ptr; uint64_t bytes; } mine[3] = {
+        {dq_weight, 4u * d}, {dk_weight, 4u * d}, {workspace, workspace_bytes}};
+    const struct { const void* ptr; uint64_t bytes; } given[4] = {
+        {q_weight, 2u * d}, {k_weight, 2u * d},
+        {rot_dim > 0 ? positions : nullptr, (uint64_t)num_axes * T * 4}, {rot_dim > 0 ? inv_freq : nullptr, 2u * rot_dim}};
+    const fa::Rows rows[6] = {grad[0], grad[1], in[0], in[1], out[0], out[1]};
+    for (int i = 0; i < 3; ++i) {
+      for (int j = i + 1; j < 3; ++j)
+        if (fa::overlaps(mine[i].ptr, mine[i].bytes, mine[j].ptr, mine[j].bytes)) return FA_ERR_INVALID_ARG;
+      for (const auto& g : given)
+        if (fa::overlaps(mine[i].ptr, mine[i].bytes, g.ptr, g.bytes)) return FA_ERR_INVALID_ARG;
+      for (const fa::Rows& r : rows)
+        if (fa::in_rows(mine[i].ptr, mine[i].bytes, r, T, d)) return FA_ERR_INVALID_ARG;
+    }
+  }
   fa::DeviceStatus* status = nullptr;
   int sm_count = 0;
   const int rc = fa::current_device_info(&status, &sm_count);

@@ -91,6 +91,7 @@ SHARED = [
     (dict(wq=0, wk=0, rot=0), 1),                    # nothing to do
     (dict(qs=511), 1), (dict(qs=0), 1), (dict(kos=-256), 1),
     (dict(qo=at(1)), 1), (dict(ko=at(6, 512)), 1),   # an output over the other tensors
+    (dict(qo=at(4)), 1), (dict(ko=at(3)), 1), (dict(qo=at(5)), 1),
     (dict(qo=at(0, 16)), 1), (dict(qo=at(0), qos=520), 1),  # over its own input, but not in place
     (dict(d=96), 2), (dict(rot=24), 2), (dict(axes=5, sec=[16, 16, 16, 8, 8]), 2), (dict(T=1 << 31), 2),
     (dict(q=at(0, 8)), 3), (dict(qs=516), 3), (dict(kos=257), 3), (dict(wq=at(2, 2)), 3), (dict(pos=at(4, 2)), 3),
@@ -106,6 +107,8 @@ def test_rope_host_validation(lib, bwd, kw, code):  # noqa: F811
 
 @pytest.mark.parametrize("kw,code", [
     (dict(gq=0), 1), (dict(gks=128), 1), (dict(dwq=0), 1), (dict(dwk=0), 1), (dict(qo=at(9)), 1),
+    (dict(dwk=at(10, 256)), 1), (dict(dwq=at(12, 4096)), 1), (dict(ws=at(7)), 1), (dict(dwq=at(8, 64)), 1),
+    (dict(dwk=at(2)), 1), (dict(ws=at(4)), 1),
     (dict(gk=at(9, 8)), 3), (dict(dwq=at(10, 2)), 3),
 ])
 def test_rope_bwd_host_validation(lib, kw, code):  # noqa: F811
