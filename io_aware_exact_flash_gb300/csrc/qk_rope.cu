@@ -396,7 +396,15 @@ int plan_rope(RopeParams& p, int64_t T, int Hq, int Hkv, int d, int sm_count) {
   p.steps[0] = (Hq + per_step - 1) / per_step;
   p.steps[1] = (Hkv + per_step - 1) / per_step;
   const int total = p.steps[0] + p.steps[1];
-  const int64_t most = (int64_t)sm_count * Tune::kBlocks * kRopeWarps;
+  int64_t most = (int64_t)sm_count * Tune::kBlocks * kRopeWarps;
+  if (!(BWD && NORM)) {
+    // Large calls take up to four times the resident warps, each with at least eight steps: warps that the
+    // memory serves late then hold up less (16384 tokens of 40 heads, d = 128, forward: 69.6 to 63.5 us).
+    // With fewer steps a warp's set-up outweighs that (8192 tokens of 32 heads: 28.7 against 32.8 us with
+    // four times the warps). With the weights' sums, every CTA adds a row to add up: 100 us either way.
+    const int64_t waves = T * total / (8 * most);
+    most *= waves < 1 ? 1 : waves > 4 ? 4 : waves;
+  }
   const int64_t per_token = T > 0 ? most / T : 1;  // warps there are for each token
   int64_t want[2];
   for (int x = 0; x < 2; ++x) {
