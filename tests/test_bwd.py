@@ -339,3 +339,69 @@ def test_bwd_python_refusals():
         with pytest.raises(fa.FaError) as e:
             fa.fa_bwd(**{**good, **kw})
         assert e.value.code == 1
+
+
+@pytest.mark.gpu
+def test_bwd_long_sequence_sampled():
+    """20011 tokens: gradients of sampled queries and keys against the formulas in fp64, row by row and
+    column by column, within the bounds above (the sums are longer: n 2^-24 with n = 20011 is 2^-9.7 of the
+    magnitudes, so SMALL counts twice here)."""
+    import io_aware_exact_flash_gb300 as fa
+
+    S, Hq, d = 20011, 2, 128
+    q, k, v, do, _ = inputs(1, S, Hq, 1, d)
+    scale = 1.0 / math.sqrt(d)
+    o, lse = fa.fa_fwd(q, k, v, causal=True, scale=scale)
+    dq, dk, dv = fa.fa_bwd(q, k, v, o, lse, do, causal=True, scale=scale)
+    Q, O, DO = (t[0].double() for t in (q, o, do))
+    K, V, L = k[0, :, 0].double(), v[0, :, 0].double(), lse[0].double()
+    delta, dabs = (DO * O).sum(-1), (DO * O).abs().sum(-1)
+    idx = torch.arange(S, device="cuda")
+    for i in (0, 1, 127, 128, 5000, 12800, S - 1):
+        for h in range(Hq):
+            p = torch.exp(K[:i + 1] @ Q[i, h] * scale - L[i, h])
+            ds = p * (V[:i + 1] @ DO[i, h] - delta[i, h])
+            mag = p * (V[:i + 1].abs() @ DO[i, h].abs() + dabs[i, h])
+            want = ds @ K[:i + 1] * scale
+            w = U * ds.abs() + 2 * SMALL * (ds.abs() + mag / 16)
+            tol = w @ K[:i + 1].abs() * scale + U * want.abs()
+            assert ((dq[0, i, h].double() - want).abs() <= tol + 1e-30).all(), f"dq row {i}"
+    for j in (0, 1, 126, 129, 5001, 12799, S - 2, S - 1):
+        want_k = torch.zeros(d, dtype=torch.float64, device="cuda")
+        want_v, tol_k, tol_v = want_k.clone(), want_k.clone(), want_k.clone()
+        for h in range(Hq):
+            p = torch.where(idx >= j, torch.exp(Q[:, h] @ K[j] * scale - L[:, h]), 0.0)
+            ds = p * (DO[:, h] @ V[j] - delta[:, h])
+            mag = p * (DO[:, h].abs() @ V[j].abs() + dabs[:, h])
+            want_v += p @ DO[:, h]
+            want_k += ds @ Q[:, h] * scale
+            tol_v += (U + 2 * SMALL) * (p @ DO[:, h].abs())
+            tol_k += (U * ds.abs() + 2 * SMALL * (ds.abs() + mag / 16)) @ Q[:, h].abs() * scale
+        assert ((dk[0, j, 0].double() - want_k).abs() <= tol_k + U * want_k.abs() + 1e-30).all(), f"dk row {j}"
+        assert ((dv[0, j, 0].double() - want_v).abs() <= tol_v + U * want_v.abs() + 1e-30).all(), f"dv row {j}"
+
+
+@pytest.mark.gpu
+def test_bwd_offsets_past_32_bits():
+    """A batch whose tensors have more than 2^31 elements (4.3 GB each): the first and the last entries."""
+    import io_aware_exact_flash_gb300 as fa
+
+    B, S, H, d = 8200, 128, 16, 128
+    assert B * S * H * d > 1 << 31
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    big = [torch.zeros(B, S, H, d, device="cuda", dtype=torch.bfloat16) for _ in range(5)]
+    lse = torch.zeros(B, S, H, device="cuda")
+    scale = 1.0 / math.sqrt(d)
+    ends = {}
+    for b in (0, B - 1):
+        q, k, v, do, _ = inputs(1, S, H, H, d, seed=b)
+        o, l = fa.fa_fwd(q, k, v, causal=True, scale=scale)
+        ends[b] = (q, k, v, o, l, do)
+        for t, x in zip(big, (q, k, v, o, do)):
+            t[b] = x[0]
+        lse[b] = l[0]
+    grads = fa.fa_bwd(big[0], big[1], big[2], big[3], lse, big[4], causal=True, scale=scale)
+    for b, (q, k, v, o, l, do) in ends.items():
+        check([g[b:b + 1] for g in grads], q, k, v, o, l, do, None, True, scale, f"entry {b}")
+    assert not any(g[1:B - 1].any() for g in grads)

@@ -207,3 +207,33 @@ def test_zero_and_non_finite_heads_stay_apart():
     touched[4, 3] = touched[5, 2] = touched[6, 1] = True
     assert torch.equal(y[~touched], clean[~touched])
     assert torch.isnan(y[6, 1]).all()
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """More than 2^31 elements of queries: the last tokens give the bits of a call on them alone."""
+    import io_aware_exact_flash_gb300 as fa
+
+    T, Hq, d = 525000, 32, 128
+    assert T * Hq * d > 1 << 31
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    q = torch.zeros(T, Hq, d, device="cuda", dtype=torch.bfloat16)
+    k = torch.zeros(T, 1, d, device="cuda", dtype=torch.bfloat16)
+    qs, ks, a, dyq, dyk = make(700, Hq, 1, d, d, 1, True)
+    q[-700:], k[-700:] = qs, ks
+    pos = torch.zeros(T, dtype=torch.int32, device="cuda")
+    pos[-700:] = a["positions"]
+    want = fa.fa_qk_norm_rope(qs, ks, **a)
+    got = fa.fa_qk_norm_rope(q, k, **{**a, "positions": pos})
+    assert torch.equal(got[0][-700:], want[0]) and torch.equal(got[1][-700:], want[1])
+    assert not got[0][:-700].any()
+    del got
+    dq = torch.zeros_like(q)
+    dq[-700:] = dyq
+    dk = torch.zeros_like(k)
+    dk[-700:] = dyk
+    wantb = fa.fa_qk_norm_rope_bwd(dyq, dyk, qs, ks, **a)
+    res = fa.fa_qk_norm_rope_bwd(dq, dk, q, k, dq=dq, dk=dk, **{**a, "positions": pos})
+    assert torch.equal(res[0][-700:], wantb[0]) and torch.equal(res[1][-700:], wantb[1])
+    assert not res[0][:-700].any()
