@@ -205,22 +205,22 @@ def _handle(index, stream):
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
-def _result(name, t, like_shape, dtype, index):
+def _result(name, t, shape, dtype, device):
     """A caller-given output after its checks, or a new one."""
     if t is None:
-        return torch.empty(like_shape, dtype=dtype, device=torch.device("cuda", index))
-    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.get_device() != index or t.shape != like_shape
+        return torch.empty(shape, dtype=dtype, device=device)
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or t.shape != shape
             or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(like_shape)} on cuda:{index}")
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t
 
 
-def _scratch(workspace, need, index):
+def _scratch(workspace, need, device):
     """A caller-given workspace (any contiguous CUDA tensor), or a new one; with its size in bytes."""
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
-    elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != index or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -255,11 +255,12 @@ def fa_bwd(q, k, v, out, lse, dout, causal=False, scale=None, dlse=None, dq=None
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     lib = load_library()
     with _on_device(index, stream):
-        dq = _result("dq", dq, q.shape, q.dtype, index)
-        dk = _result("dk", dk, k.shape, k.dtype, index)
-        dv = _result("dv", dv, v.shape, v.dtype, index)
+        device = q.device
+        dq = _result("dq", dq, q.shape, q.dtype, device)
+        dk = _result("dk", dk, k.shape, k.dtype, device)
+        dv = _result("dv", dv, v.shape, v.dtype, device)
         need = 0 if workspace is not None else fa_bwd_workspace_bytes(B, Hq, Hkv, S, d, causal)
-        workspace, ws_bytes = _scratch(workspace, need, index)
+        workspace, ws_bytes = _scratch(workspace, need, device)
         code = lib.fa_bwd(_address(q), _address(k), _address(v), _address(out), _address(lse), _address(dout),
                           _address(dlse), _address(dq), _address(dk), _address(dv), B, Hq, Hkv, S, d,
                           int(bool(causal)), scale, _address(workspace), ws_bytes, _handle(index, stream))
@@ -421,30 +422,36 @@ def fa_paged_append(k_new, v_new, cu_seqlens_new, kv_lens_before, page_table, k_
     _check("fa_paged_append", code)
 
 
-def _token_rows(name, t, shape=None, index=None):
+def _token_rows(name, t, shape, width, index):
     """Checks a [T, heads, d] bf16 CUDA tensor whose heads are contiguous within a token (a view of a
-    fused projection, for instance); returns its token stride in elements."""
+    fused projection, for instance); width: heads * d. Returns its token stride in elements."""
     if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA bfloat16 tensor")
-    if shape is not None and t.shape != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be of shape {tuple(shape)}")
-    if index is not None and t.get_device() != index:
+    if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+    if t.is_contiguous():
+        return width
+    s_t, s_h, s_d = t.stride()
+    T, H, d = shape
+    if (d > 1 and s_d != 1) or (H > 1 and s_h != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return s_t if T > 1 else width
+
+
+def _tokens(name, t):
+    """The shape of a [T, heads, d] argument."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA bfloat16 tensor")
     if t.dim() != 3:
         raise ValueError(f"{name} must be [T, heads, d]")
-    T, H, d = t.shape
-    s_t, s_h, s_d = t.stride()
-    if T > 0 and ((d > 1 and s_d != 1) or (H > 1 and s_h != d)):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return s_t if T > 1 else H * d
+    return t.shape
 
 
-def _rope_arguments(q, k, index, positions, inv_freq, q_weight, k_weight, sections):
+def _rope_arguments(T, d, index, positions, inv_freq, q_weight, k_weight, sections):
     """Checks the arguments that fa_qk_norm_rope and its backward share; returns (num_axes, sections as a
     host array, rot_dim)."""
-    T, _, d = q.shape
-    if k.shape[0] != T or k.shape[2] != d:
-        raise ValueError("q and k must be [T, Hq, d] and [T, Hkv, d]")
     if (q_weight is None) != (k_weight is None):
         raise ValueError("q_weight and k_weight go together")
     if q_weight is not None:
@@ -486,21 +493,24 @@ def fa_qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight
     [pairs] fp32, where 2 * pairs elements of each head are rotated; both None: norm only.
     interleaved: pairs are (2i, 2i + 1) instead of (i, i + pairs). q_out may be q and k_out k (in
     place). Returns (q_out, k_out)."""
-    sq = _token_rows("q", q)
-    index = q.get_device()
-    sk = _token_rows("k", k, None, index)
-    num_axes, host_sections, rot_dim = _rope_arguments(q, k, index, positions, inv_freq, q_weight, k_weight, sections)
-    T, Hq, d = q.shape
+    q_shape, k_shape = _tokens("q", q), _tokens("k", k)
+    T, Hq, d = q_shape
+    Hkv = k_shape[1]
+    if k_shape[0] != T or k_shape[2] != d:
+        raise ValueError("q and k must be [T, Hq, d] and [T, Hkv, d]")
+    index, wq, wk = q.get_device(), Hq * d, Hkv * d
+    sq, sk = _token_rows("q", q, q_shape, wq, index), _token_rows("k", k, k_shape, wk, index)
+    num_axes, host_sections, rot_dim = _rope_arguments(T, d, index, positions, inv_freq, q_weight, k_weight, sections)
     lib = load_library()
     with _on_device(index, stream):
         if q_out is None:
             q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         if k_out is None:
             k_out = torch.empty(k.shape, dtype=k.dtype, device=q.device)
-        so, sp = _token_rows("q_out", q_out, q.shape, index), _token_rows("k_out", k_out, k.shape, index)
+        so, sp = _token_rows("q_out", q_out, q_shape, wq, index), _token_rows("k_out", k_out, k_shape, wk, index)
         code = lib.fa_qk_norm_rope(_address(q), sq, _address(k), sk, _address(q_weight), _address(k_weight), eps,
                                    _address(positions), _address(inv_freq), num_axes, host_sections, rot_dim,
-                                   int(bool(interleaved)), T, Hq, k.shape[1], d, _address(q_out), so,
+                                   int(bool(interleaved)), T, Hq, Hkv, d, _address(q_out), so,
                                    _address(k_out), sp, _handle(index, stream))
     _check("fa_qk_norm_rope", code)
     return q_out, k_out
@@ -516,26 +526,29 @@ def fa_qk_norm_rope_bwd(dq_out, dk_out, q, k, positions=None, inv_freq=None, q_w
     """Gradients of fa_qk_norm_rope: dq_out, dk_out are those of its results, q and k its inputs (not
     read without weights). Returns (dq, dk, dq_weight, dk_weight): bf16 like q and k, and fp32 [d]
     (None without weights). dq may be dq_out and dk dk_out (in place)."""
-    sq = _token_rows("q", q)
-    index = q.get_device()
-    sk = _token_rows("k", k, None, index)
-    sg, sh = _token_rows("dq_out", dq_out, q.shape, index), _token_rows("dk_out", dk_out, k.shape, index)
-    num_axes, host_sections, rot_dim = _rope_arguments(q, k, index, positions, inv_freq, q_weight, k_weight, sections)
-    T, Hq, d = q.shape
-    Hkv = k.shape[1]
+    q_shape, k_shape = _tokens("q", q), _tokens("k", k)
+    T, Hq, d = q_shape
+    Hkv = k_shape[1]
+    if k_shape[0] != T or k_shape[2] != d:
+        raise ValueError("q and k must be [T, Hq, d] and [T, Hkv, d]")
+    index, wq, wk = q.get_device(), Hq * d, Hkv * d
+    sq, sk = _token_rows("q", q, q_shape, wq, index), _token_rows("k", k, k_shape, wk, index)
+    sg, sh = _token_rows("dq_out", dq_out, q_shape, wq, index), _token_rows("dk_out", dk_out, k_shape, wk, index)
+    num_axes, host_sections, rot_dim = _rope_arguments(T, d, index, positions, inv_freq, q_weight, k_weight, sections)
     lib = load_library()
     with _on_device(index, stream):
         if dq is None:
             dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         if dk is None:
             dk = torch.empty(k.shape, dtype=k.dtype, device=q.device)
-        so, sp = _token_rows("dq", dq, q.shape, index), _token_rows("dk", dk, k.shape, index)
+        so, sp = _token_rows("dq", dq, q_shape, wq, index), _token_rows("dk", dk, k_shape, wk, index)
         ws_bytes = 0
         if q_weight is not None:
-            dq_weight = _result("dq_weight", dq_weight, q_weight.shape, torch.float32, index)
-            dk_weight = _result("dk_weight", dk_weight, k_weight.shape, torch.float32, index)
+            device = q.device
+            dq_weight = _result("dq_weight", dq_weight, q_weight.shape, torch.float32, device)
+            dk_weight = _result("dk_weight", dk_weight, k_weight.shape, torch.float32, device)
             need = 0 if workspace is not None else fa_qk_norm_rope_bwd_workspace_bytes(T, Hq, Hkv, d)
-            workspace, ws_bytes = _scratch(workspace, need, index)
+            workspace, ws_bytes = _scratch(workspace, need, device)
         else:
             dq_weight = dk_weight = workspace = None
         code = lib.fa_qk_norm_rope_bwd(_address(dq_out), sg, _address(dk_out), sh, _address(q), sq, _address(k), sk,
