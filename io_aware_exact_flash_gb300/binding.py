@@ -456,7 +456,8 @@ def _rope_arguments(T, d, index, positions, inv_freq, q_weight, k_weight, sectio
         raise ValueError("q_weight and k_weight go together")
     if q_weight is not None:
         for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-            if w.dtype != torch.bfloat16 or w.shape != (d,) or w.get_device() != index or not w.is_contiguous():
+            if (not isinstance(w, torch.Tensor) or w.dtype != torch.bfloat16 or w.shape != (d,)
+                    or w.get_device() != index or not w.is_contiguous()):
                 raise ValueError(f"{name} must be a contiguous bfloat16 tensor of {d} elements on cuda:{index}")
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq go together")
@@ -464,11 +465,11 @@ def _rope_arguments(T, d, index, positions, inv_freq, q_weight, k_weight, sectio
         if q_weight is None:
             raise ValueError("nothing to do: neither weights nor positions")
         return 1, None, 0
-    if (inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or inv_freq.get_device() != index
-            or not inv_freq.is_contiguous()):
+    if (not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != torch.float32 or inv_freq.dim() != 1
+            or inv_freq.get_device() != index or not inv_freq.is_contiguous()):
         raise ValueError(f"inv_freq must be a contiguous 1-D float32 tensor on cuda:{index}")
-    axes_of = positions.dim()
-    if (positions.dtype != torch.int32 or axes_of not in (1, 2) or positions.shape[-1] != T
+    axes_of = positions.dim() if isinstance(positions, torch.Tensor) else 0
+    if (axes_of not in (1, 2) or positions.dtype != torch.int32 or positions.shape[-1] != T
             or positions.get_device() != index or not positions.is_contiguous()):
         raise ValueError(f"positions must be a contiguous int32 tensor [T] or [axes, T] on cuda:{index}, T = {T}")
     num_axes = 1 if axes_of == 1 else positions.shape[0]

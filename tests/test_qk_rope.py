@@ -237,3 +237,67 @@ def test_offsets_past_32_bits():
     res = fa.fa_qk_norm_rope_bwd(dq, dk, q, k, dq=dq, dk=dk, **{**a, "positions": pos})
     assert torch.equal(res[0][-700:], wantb[0]) and torch.equal(res[1][-700:], wantb[1])
     assert not res[0][:-700].any()
+
+
+@pytest.mark.gpu
+def test_python_refusals():
+    import io_aware_exact_flash_gb300 as fa
+
+    q, k, a, dq_out, dk_out = make(9, 4, 2, 64, 64, 2, True)
+    forward = dict(q=q, k=k, **a)
+    backward = dict(dq_out=dq_out, dk_out=dk_out, **forward)
+    types = (dict(q=q.half()), dict(k=k.cpu()), dict(q=[1]))
+    values = (dict(k=k[:5]), dict(k=k[0]), dict(q=q.transpose(0, 1).contiguous().transpose(0, 1)), dict(q_weight=None),
+              dict(k_weight=[1.0] * 64), dict(q_weight=a["q_weight"].float()), dict(q_weight=a["q_weight"][:32]),
+              dict(positions=None), dict(inv_freq=None), dict(positions=a["positions"].long()),
+              dict(positions=a["positions"][:, :5]), dict(positions=[1, 2]), dict(inv_freq=a["inv_freq"].double()),
+              dict(inv_freq=0.5), dict(inv_freq=a["inv_freq"].cpu()), dict(sections=None), dict(sections=[32]),
+              dict(sections=[16, 17]), dict(sections=[33, -1]),
+              dict(q_weight=None, k_weight=None, positions=None, inv_freq=None, sections=None))
+    for call, good in ((fa.fa_qk_norm_rope, forward), (fa.fa_qk_norm_rope_bwd, backward)):
+        for kw in types:
+            with pytest.raises(TypeError):
+                call(**{**good, **kw})
+        for kw in values:
+            with pytest.raises(ValueError):
+                call(**{**good, **kw})
+        for kw in (dict(eps=0.0), dict(eps=float("nan"))):
+            with pytest.raises(fa.FaError) as e:
+                call(**{**good, **kw})
+            assert e.value.code == 1
+    for kw in (dict(q_out=k), dict(q_out=q[:, :2]), dict(k_out=q)):
+        with pytest.raises(ValueError):
+            fa.fa_qk_norm_rope(**{**forward, **kw})
+    for kw in (dict(dq=dk_out), dict(dq_weight=torch.empty(64, device="cuda").double()), dict(dk_out=dk_out[:5]),
+               dict(workspace=torch.empty(4096, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            fa.fa_qk_norm_rope_bwd(**{**backward, **kw})
+    with pytest.raises(fa.FaError) as e:
+        fa.fa_qk_norm_rope_bwd(**backward, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    assert e.value.code == 4  # FA_ERR_WORKSPACE
+
+
+@pytest.mark.gpu
+def test_two_streams_and_a_graph_agree_with_one_call():
+    import io_aware_exact_flash_gb300 as fa
+
+    cases = [make(T, 8, 2, 64, 32, 1, True, seed=T) for T in (301, 77)]
+    run = lambda c, **kw: (fa.fa_qk_norm_rope(c[0], c[1], **c[2], **kw)  # noqa: E731
+                           + fa.fa_qk_norm_rope_bwd(c[3], c[4], c[0], c[1], **c[2], **kw))
+    want = [run(c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[run(c, stream=s) for c, s in zip(cases, streams)] for _ in range(5)]
+    graphs, results = [], []
+    for c in cases:  # each graph has its own memory
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            results.append(run(c))
+    for _ in range(2):
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for turn in got + [results]:
+        for have, expected in zip(turn, want):
+            assert all(torch.equal(x, y) for x, y in zip(have, expected))
