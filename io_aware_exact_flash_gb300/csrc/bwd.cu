@@ -22,7 +22,8 @@
 //   warps 4-11  two warpgroups; thread t of a warpgroup owns row t of the 128 x 128 score tile
 //               (a TMEM lane), warpgroup g its columns [64 g, 64 g + 64)
 // P and dS are rounded to bf16 (the input type, as in the forward pass's P V) for their matrix
-// products, and written back to TMEM as the A operands; sums and statistics stay in fp32.
+// products, and written back to TMEM as the A operands; sums and statistics stay in fp32. Sequences of
+// few tokens keep what the rounding takes away as a second bf16 operand and add its products too.
 #include <cuda_bf16.h>
 #include <atomic>
 #include <cmath>
@@ -91,6 +92,13 @@ struct alignas(64) BwdParams {
   float scale, scale_log2;
   DeviceStatus* status;
 };
+
+// Up to this many tokens P and dS are multiplied as two bf16 operands each. A gradient that sums few terms
+// inherits their roundings one to one: relative errors of 0.0021 to 0.0030 with one to four tokens, where a
+// result that is rounded once has 0.0017 and many terms settle at 0.0024. The price is 1 to 2 us, in calls
+// that take 12 to 14 (8 heads of 1 or 16 tokens); for 16 x 128 tokens of 64 heads it would be 57 to 65 us, for
+// 4 x 4096 of 32 1186 to 1593.
+constexpr int kSplitTokens = 16;
 
 struct StatParams {
   const __nv_bfloat16 *o, *dout;  // [B, S, Hq, d]
@@ -178,14 +186,26 @@ __device__ __forceinline__ void mma_scores(uint32_t d_tmem, uint64_t a_desc, uin
 
 // acc[128 x d] += A B: A (bf16 pairs) in TMEM, 16 columns of the score tile per step. Each
 // warpgroup writes its 64 columns' pairs over the first half of its own 64 TMEM columns, so the
-// second half of A starts 64 columns in. B is the streamed tile as the MN-major operand.
-template <int D>
+// second half of A starts 64 columns in. B is the streamed tile as the MN-major operand. SPLIT: the
+// rest of A (see `rest_bf16x2`) lies in the second half of the 64 columns.
+template <int D, bool SPLIT>
 __device__ __forceinline__ void mma_accumulate(uint32_t acc, uint32_t a_tmem, uint64_t b_desc, bool accumulate) {
   constexpr uint32_t idesc = make_idesc_bf16(kTile, D, true);
 #pragma unroll
   for (int kk = 0; kk < kTile / 16; ++kk)
     mma_ts(acc, a_tmem + kk * 8 + (kk >> 2) * 32, b_desc + (uint64_t)kk * (2048 >> 4), idesc,
            (kk > 0 || accumulate) ? 1u : 0u);
+  if constexpr (SPLIT) {
+#pragma unroll
+    for (int kk = 0; kk < kTile / 16; ++kk)
+      mma_ts(acc, a_tmem + 32 + kk * 8 + (kk >> 2) * 32, b_desc + (uint64_t)kk * (2048 >> 4), idesc, 1u);
+  }
+}
+
+// What the rounding of a and b to the bf16 pair `rounded` took away (exact in fp32), rounded to bf16 itself:
+// the two operands together hold P and dS to 2^-16.
+__device__ __forceinline__ uint32_t rest_bf16x2(float a, float b, uint32_t rounded) {
+  return pack_bf16x2(a - __uint_as_float(rounded << 16), b - __uint_as_float(rounded & 0xffff0000u));
 }
 
 __device__ __forceinline__ void st_global_32(void* dst, const uint32_t* v) {
@@ -381,7 +401,7 @@ __device__ __forceinline__ void drain_copies(const BwdParams& p, Ctl<D>& ctl, co
 // registers, and one elected lane issues each product: issued from a loop that only one lane runs,
 // every tcgen05.mma took about 100 cycles to issue (64 to execute) and the loop was bound by that;
 // with one such warp for both chains its waits and commits still left the tensor core idle.
-template <int D, bool KEY, int CHAIN>
+template <int D, bool SPLIT, bool KEY, int CHAIN>
 __device__ __forceinline__ void issue_mmas(const BwdParams& p, int n, uint8_t* smem, Ctl<D>& ctl, int r, int first,
                                            bool same) {
   using C = BwdCfg<D>;
@@ -438,7 +458,7 @@ __device__ __forceinline__ void issue_mmas(const BwdParams& p, int n, uint8_t* s
     __syncwarp();
     tc_fence_after();
     if (elect_one()) {
-      mma_accumulate<D>(tmem + acc, tmem + a_col, bm + (uint64_t)(slot * (TB >> 4)), add);
+      mma_accumulate<D, SPLIT>(tmem + acc, tmem + a_col, bm + (uint64_t)(slot * (TB >> 4)), add);
       mma_commit(&bars.empty[slot]);
     }
     __syncwarp();
@@ -503,7 +523,7 @@ __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t* r) 
 }
 
 // P and dS of one row's 64 columns per step, then the gradients' epilogue.
-template <int D, bool KEY>
+template <int D, bool SPLIT, bool KEY>
 __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u, uint8_t* smem, Ctl<D>& ctl, int r,
                                            int first) {
   using C = BwdCfg<D>;
@@ -564,7 +584,7 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t pk[16];
+        uint32_t pk[16], rest[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           const uint32_t* v = sr + 32 * h + 2 * k;
@@ -574,8 +594,10 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
           x1 = ex2(x1);
           pr[16 * h + k] = f32x2(x0, x1);
           pk[k] = pack_bf16x2(x0, x1);
+          if constexpr (SPLIT) rest[k] = rest_bf16x2(x0, x1, pk[k]);
         }
         tmem_st_frag(ts + ((16u * h) << 16), pk);  // P^T is dV's A operand, written over the scores
+        if constexpr (SPLIT) tmem_st_frag(ts + ((16u * h) << 16) + 32, rest);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -616,7 +638,7 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
       tmem_ld_wait(dr + 32);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t pk[16];
+        uint32_t pk[16], rest[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           const uint32_t* v = dr + 32 * h + 2 * k;
@@ -624,8 +646,10 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
           split_f32x2(mul_f32x2(pr[16 * h + k], add_f32x2(f32x2(__uint_as_float(v[0]), __uint_as_float(v[1])),
                                                           nd[k >> 1])), a, b);
           pk[k] = pack_bf16x2(a, b);
+          if constexpr (SPLIT) rest[k] = rest_bf16x2(a, b, pk[k]);
         }
         tmem_st_frag(td + ((16u * h) << 16), pk);  // dS^T over dP^T
+        if constexpr (SPLIT) tmem_st_frag(td + ((16u * h) << 16) + 32, rest);
       }
     } else {
       uint32_t dr[64];
@@ -633,7 +657,7 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
       tmem_ld32(td + 32, dr + 32);
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) {
-        uint32_t pk[16];
+        uint32_t pk[16], rest[16];
         tmem_ld_wait(dr + 32 * cc);
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
@@ -642,8 +666,10 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
           split_f32x2(mul_f32x2(pr[16 * cc + k], add_f32x2(f32x2(__uint_as_float(v[0]), __uint_as_float(v[1])),
                                                            ndelta2)), a, b);
           pk[k] = pack_bf16x2(a, b);
+          if constexpr (SPLIT) rest[k] = rest_bf16x2(a, b, pk[k]);
         }
         tmem_st16(ts + 16 * cc, pk);  // dS over the scores
+        if constexpr (SPLIT) tmem_st16(ts + 32 + 16 * cc, rest);
       }
     }
     tmem_st_wait();
@@ -745,7 +771,7 @@ __device__ __forceinline__ int walk_units(const BwdParams& p, Ctl<D>& ctl, F f) 
   return r;
 }
 
-template <int D>
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kBwdThreads, 1) bwd_kernel(const __grid_constant__ BwdParams p) {
   using C = BwdCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -817,15 +843,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) bwd_kernel(const __grid_consta
   } else if (warp == 1) {
     regs_dec<kRegsBwdControl>();
     const int units = walk_units<D>(p, ctl, [&](const BwdUnit& u, int r, int first, bool same) {
-      if (u.key) issue_mmas<D, true, 0>(p, u.steps, smem, ctl, r, first, same);
-      else issue_mmas<D, false, 0>(p, u.steps, smem, ctl, r, first, same);
+      if (u.key) issue_mmas<D, SPLIT, true, 0>(p, u.steps, smem, ctl, r, first, same);
+      else issue_mmas<D, SPLIT, false, 0>(p, u.steps, smem, ctl, r, first, same);
     });
     wait_products<D>(p, ctl, units);
   } else if (warp == 2) {
     regs_dec<kRegsBwdControl>();
     const int units = walk_units<D>(p, ctl, [&](const BwdUnit& u, int r, int first, bool same) {
-      if (u.key) issue_mmas<D, true, 1>(p, u.steps, smem, ctl, r, first, same);
-      else issue_mmas<D, false, 1>(p, u.steps, smem, ctl, r, first, same);
+      if (u.key) issue_mmas<D, SPLIT, true, 1>(p, u.steps, smem, ctl, r, first, same);
+      else issue_mmas<D, SPLIT, false, 1>(p, u.steps, smem, ctl, r, first, same);
     });
     wait_products<D>(p, ctl, units);
   } else if (warp == 3) {
@@ -833,8 +859,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) bwd_kernel(const __grid_consta
   } else {
     regs_inc<kRegsBwdMath>();
     walk_units<D>(p, ctl, [&](const BwdUnit& u, int r, int first, bool) {
-      if (u.key) math_warps<D, true>(p, u, smem, ctl, r, first);
-      else math_warps<D, false>(p, u, smem, ctl, r, first);
+      if (u.key) math_warps<D, SPLIT, true>(p, u, smem, ctl, r, first);
+      else math_warps<D, SPLIT, false>(p, u, smem, ctl, r, first);
     });
   }
   tc_fence_before();
@@ -915,13 +941,13 @@ __global__ void __launch_bounds__(kStatThreads) bwd_stat_kernel(StatParams p) {
   dst[128] = ndelta;
 }
 
-template <int D>
+template <int D, bool SPLIT>
 cudaError_t launch_bwd(const StatParams& sp, const BwdParams& p, int64_t units, cudaStream_t stream) {
   static std::atomic<int> pool_ok{-1};
   if (pool_ok.load(std::memory_order_relaxed) < 0) {
     // the register split draws on the registers the CTA launches with
     cudaFuncAttributes attr;
-    cudaError_t e = cudaFuncGetAttributes(&attr, bwd_kernel<D>);
+    cudaError_t e = cudaFuncGetAttributes(&attr, bwd_kernel<D, SPLIT>);
     if (e != cudaSuccess) return e;
     pool_ok.store(attr.numRegs * kBwdThreads >= 128 * kRegsBwdControl + 256 * kRegsBwdMath ? 1 : 0,
                   std::memory_order_relaxed);
@@ -932,7 +958,7 @@ cudaError_t launch_bwd(const StatParams& sp, const BwdParams& p, int64_t units, 
   cudaGetDevice(&dev);
   if (dev >= 32 || !(configured_mask.load(std::memory_order_acquire) & (1u << dev))) {
     cudaError_t e =
-        cudaFuncSetAttribute(bwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdCfg<D>::kSmemBytes);
+        cudaFuncSetAttribute(bwd_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdCfg<D>::kSmemBytes);
     if (e != cudaSuccess) return e;
     if (dev < 32) configured_mask.fetch_or(1u << dev, std::memory_order_release);
   }
@@ -952,7 +978,7 @@ cudaError_t launch_bwd(const StatParams& sp, const BwdParams& p, int64_t units, 
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, bwd_kernel<D>, p);
+  e = cudaLaunchKernelEx(&cfg, bwd_kernel<D, SPLIT>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -1051,6 +1077,9 @@ extern "C" fa_status fa_bwd(const void* q, const void* k, const void* v, const v
   sp.T = p.T;
   sp.Hq = Hq;
   const int64_t units = (int64_t)p.T * B * ((int64_t)Hq + Hkv);
-  const cudaError_t e = d == 128 ? fa::launch_bwd<128>(sp, p, units, stream) : fa::launch_bwd<64>(sp, p, units, stream);
+  const bool split = S <= fa::kSplitTokens;
+  const auto launch = d == 128 ? (split ? fa::launch_bwd<128, true> : fa::launch_bwd<128, false>)
+                               : (split ? fa::launch_bwd<64, true> : fa::launch_bwd<64, false>);
+  const cudaError_t e = launch(sp, p, units, stream);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

@@ -24,7 +24,7 @@ U = 2.0 ** -8
 SMALL = 2.0 ** -10
 
 
-def reference(q, k, v, o, lse, do, dlse, causal, scale):
+def reference(q, k, v, o, lse, do, dlse, causal, scale, u=U, small=SMALL):
     """Gradients in fp64 and, for each, the bound on the kernel's error stated above."""
     q, k, v, o, lse, do = (t.double() for t in (q, k, v, o, lse, do))
     B, S, Hq, d = q.shape
@@ -50,10 +50,10 @@ def reference(q, k, v, o, lse, do, dlse, causal, scale):
     dv = to_kv(torch.einsum("bhij,bihd->bjhd", p, do))
     dq, dk = dqk(ds)
     ka, qa = ke.abs(), q.abs()
-    w = U * ds.abs() + SMALL * (ds.abs() + mag / 16)
+    w = (u + small) * ds.abs() + 2.0 ** -14 * mag
     tq = torch.einsum("bhij,bjhd->bihd", w, ka) * scale
     tk = to_kv(torch.einsum("bhij,bihd->bjhd", w, qa)) * scale
-    tv = (U + SMALL) * to_kv(torch.einsum("bhij,bihd->bjhd", p, do.abs()))
+    tv = (u + small) * to_kv(torch.einsum("bhij,bihd->bjhd", p, do.abs()))
     return (dq, dk, dv), (tq + U * dq.abs(), tk + U * dk.abs(), tv + U * dv.abs())
 
 
@@ -114,6 +114,29 @@ def test_bwd_matches_fp64(B, S, Hq, Hkv, d, causal, with_dlse):
     grads = fa.fa_bwd(q, k, v, o, lse, do, causal=causal, scale=scale, dlse=dlse)
     assert fa.fa_get_device_status() == (0, 0)
     check(grads, q, k, v, o, lse, do, dlse, causal, scale, f"bwd {B, S, Hq, Hkv, d, causal}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("B,S,Hq,Hkv", [(3, 1, 4, 2), (5, 2, 6, 2), (1, 3, 8, 1), (150, 4, 4, 2), (2, 9, 4, 4),
+                                        (20, 16, 12, 6)])
+def test_bwd_of_few_tokens_rounds_once(B, S, Hq, Hkv, d, causal):
+    """Up to 16 tokens P and dS are two bf16 operands each, off by at most u^2 = 2^-16 together. In the
+    bounds above that takes the place of u, and with at most 16 terms per head and 8 heads the fp32 sums add
+    less than 2^-17 of the magnitudes, so that 2^-13 covers them with the 2^-14 of P. (150 and 20 entries: more
+    units than SMs.)"""
+    import io_aware_exact_flash_gb300 as fa
+
+    q, k, v, do, dlse = inputs(B, S, Hq, Hkv, d, seed=3)
+    scale = 1.0 / math.sqrt(d)
+    o, lse = fa.fa_fwd(q, k, v, causal=causal, scale=scale)
+    grads = fa.fa_bwd(q, k, v, o, lse, do, causal=causal, scale=scale, dlse=dlse)
+    assert fa.fa_get_device_status() == (0, 0)
+    want, tol = reference(q, k, v, o, lse, do, dlse, causal, scale, u=2.0 ** -16, small=2.0 ** -13)
+    for name, got, ref, t in zip(("dq", "dk", "dv"), grads, want, tol):
+        worst = float(((got.double() - ref).abs() / (t + 1e-30)).max())
+        assert worst <= 1, f"{name} off by {worst:.2f} of its bound"
 
 
 @pytest.mark.gpu
