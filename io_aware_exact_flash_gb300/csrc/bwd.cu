@@ -15,12 +15,12 @@
 // five would do, but every gradient is summed inside one CTA in a fixed order: no atomics, the
 // same bits every run, and no fp32 dQ traffic (a 64 KB read-modify-write per tile pair).
 //
-// CTA organisation (384 threads, one CTA per SM):
+// CTA organisation (384 threads at d = 128, 640 at d = 64, one CTA per SM):
 //   warp 0      TMA producer: the two resident tiles, then the streamed tiles into a ring of slots
 //   warp 1      TMEM owner; issues the MMAs of the scores and of what P (or, for dQ, dS) multiplies
 //   warp 2      issues the MMAs of dP and, for dK, of what dS multiplies
-//   warps 4-11  two warpgroups; thread t of a warpgroup owns row t of the 128 x 128 score tile
-//               (a TMEM lane), warpgroup g its columns [64 g, 64 g + 64)
+//   warps 4...  two warpgroups (d = 64: four); thread t of a warpgroup owns row t of the 128 x 128 score
+//               tile (a TMEM lane), warpgroup g its columns [64 g, 64 g + 64) (d = 64: [32 g, 32 g + 32))
 // P and dS are rounded to bf16 (the input type, as in the forward pass's P V) for their matrix
 // products, and written back to TMEM as the A operands; sums and statistics stay in fp32. Sequences of
 // few tokens keep what the rounding takes away as a second bf16 operand and add its products too.
@@ -36,11 +36,11 @@ namespace fa {
 namespace {
 
 constexpr int kTile = 128;        // queries and keys per tile
-constexpr int kBwdThreads = 384;
 constexpr int kStatBytes = 1024;  // -LSE (base 2) and -delta of one query tile
+// Registers per thread with two math warpgroups (with four every warp keeps the 96 of the launch).
 constexpr int kRegsBwdControl = 88;
 constexpr int kRegsBwdMath = 208;
-static_assert(128 * kRegsBwdControl + 256 * kRegsBwdMath <= kBwdThreads * 168, "register split too large");
+static_assert(128 * kRegsBwdControl + 256 * kRegsBwdMath <= 384 * 168, "register split too large");
 
 enum : uint32_t {
   kSiteBwdEmpty = 30,
@@ -110,6 +110,13 @@ struct StatParams {
 template <int D>
 struct BwdCfg {
   static constexpr int kTileBytes = kTile * D * 2;
+  // Math warpgroups. At d = 64 they are the bound, and four hide more of each other's waits than two: 882
+  // against 909 us (B = 4, H = 32, S = 4096, causal), 47 against 49 us (2 x 1000 tokens, 32 over 8 heads). At
+  // d = 128 the tensor core is: 1223 against 1189 us on the long case, 69 against 67 us.
+  static constexpr int kGroups = D == 128 ? 2 : 4;
+  static constexpr int kCols = kTile / kGroups;       // score columns of each
+  static constexpr int kThreads = 128 + 128 * kGroups;
+  static constexpr int kWalkers = 3 + 4 * kGroups;    // warps that walk the units: all but warp 3
   static constexpr int kSub = D / 64;          // 128-byte-wide column blocks per tile
   static constexpr int kSubBytes = kTile * 128;
   static constexpr int kSlots = D == 128 ? 5 : 10;
@@ -139,7 +146,6 @@ struct Ctl {
   uint32_t tmem;
   int abort;
 };
-constexpr int kBwdWalkers = 11;  // warps that walk the units: 0 to 2 and 4 to 11
 
 // Which tiles a CTA owns and streams.
 struct BwdUnit {
@@ -185,20 +191,18 @@ __device__ __forceinline__ void mma_scores(uint32_t d_tmem, uint64_t a_desc, uin
 }
 
 // acc[128 x d] += A B: A (bf16 pairs) in TMEM, 16 columns of the score tile per step. Each
-// warpgroup writes its 64 columns' pairs over the first half of its own 64 TMEM columns, so the
-// second half of A starts 64 columns in. B is the streamed tile as the MN-major operand. SPLIT: the
-// rest of A (see `rest_bf16x2`) lies in the second half of the 64 columns.
+// warpgroup writes its columns' pairs over the first half of its own TMEM columns. B is the streamed
+// tile as the MN-major operand. SPLIT: the rest of A (see `rest_bf16x2`) lies in the second half.
 template <int D, bool SPLIT>
 __device__ __forceinline__ void mma_accumulate(uint32_t acc, uint32_t a_tmem, uint64_t b_desc, bool accumulate) {
   constexpr uint32_t idesc = make_idesc_bf16(kTile, D, true);
+  constexpr int kCols = BwdCfg<D>::kCols;
 #pragma unroll
-  for (int kk = 0; kk < kTile / 16; ++kk)
-    mma_ts(acc, a_tmem + kk * 8 + (kk >> 2) * 32, b_desc + (uint64_t)kk * (2048 >> 4), idesc,
-           (kk > 0 || accumulate) ? 1u : 0u);
-  if constexpr (SPLIT) {
+  for (int rest = 0; rest <= (SPLIT ? kCols / 2 : 0); rest += kCols / 2) {
 #pragma unroll
     for (int kk = 0; kk < kTile / 16; ++kk)
-      mma_ts(acc, a_tmem + 32 + kk * 8 + (kk >> 2) * 32, b_desc + (uint64_t)kk * (2048 >> 4), idesc, 1u);
+      mma_ts(acc, a_tmem + rest + kk * 8 + kk * 16 / kCols * (kCols / 2), b_desc + (uint64_t)kk * (2048 >> 4), idesc,
+             (kk > 0 || rest > 0 || accumulate) ? 1u : 0u);
   }
 }
 
@@ -504,25 +508,49 @@ __device__ __forceinline__ void issue_mmas(const BwdParams& p, int n, uint8_t* s
   __syncwarp();
 }
 
-// TMEM accesses of 16 lanes in matrix-fragment form: thread 4 a + b of the warp holds, of lanes a and
-// a + 8, the 64-bit (load: columns 8 q + 2 b, + 1) or 32-bit (store: column 4 q + b) words of each
+// TMEM accesses of 16 lanes and 64 or 32 columns in matrix-fragment form: thread 4 a + b of the warp holds, of
+// lanes a and a + 8, the 64-bit (load: columns 8 q + 2 b, + 1) or 32-bit (store: column 4 q + b) words of each
 // group q. Load: r[4 q], r[4 q + 1] of lane a, r[4 q + 2], r[4 q + 3] of lane a + 8; store: r[2 q] of
 // lane a, r[2 q + 1] of lane a + 8.
+template <int N>  // 16 or 32 words
 __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
+  if constexpr (N == 32) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+  } else {
+    static_assert(N == 16, "words per thread");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+  }
 }
+template <int N>
+__device__ __forceinline__ void frag_wait(uint32_t* r) {
+  if constexpr (N == 32) tmem_ld_wait(r);
+  else tmem_ld_wait16(r);
+}
+template <int N>  // 8 or 16 words
 __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
+  if constexpr (N == 16) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
+  } else {
+    static_assert(N == 8, "words per thread");
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
+  }
 }
 
-// P and dS of one row's 64 columns per step, then the gradients' epilogue.
+// P and dS of one row's columns (this warpgroup's share) per step, then the gradients' epilogue.
 template <int D, bool SPLIT, bool KEY>
 __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u, uint8_t* smem, Ctl<D>& ctl, int r,
                                            int first) {
@@ -535,7 +563,8 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
   const int g = (warp - 4) >> 2;
   const int row = (warp & 3) * 32 + lane;
   const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-  const uint32_t half_off = lane_off + 64 * g;
+  constexpr int kCols = C::kCols, kWords = kCols / 2;  // kWords: a thread's words of 16 lanes in fragment form
+  const uint32_t half_off = lane_off + kCols * g;
   const uint64_t c2 = f32x2(p.scale_log2, p.scale_log2);
   uint64_t nlse2 = 0, ndelta2 = 0;  // query unit: this row's statistics
   if constexpr (!KEY) {
@@ -546,76 +575,77 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
   }
   int t = u.first;
   for (int i = first; i < first + u.steps; ++i) {  // counted over the CTA's units of this kind
-    // columns [lo, hi) of this row's 64 are not masked
-    int lo = 0, hi = 64;
+    // columns [lo, hi) of this row's share are not masked
+    int lo = 0, hi = kCols;
     if (p.causal && t == u.tile) {
-      if (KEY) lo = row - 64 * g;
-      else hi = row + 1 - 64 * g;
+      if (KEY) lo = row - kCols * g;
+      else hi = row + 1 - kCols * g;
     }
-    if (!KEY && (t + 1) * kTile > p.S) hi = min(hi, p.S - t * kTile - 64 * g);
-    const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < 64);
-    // Key unit: the statistics belong to the columns. In fragment form a thread has 16 of the 64
+    if (!KEY && (t + 1) * kTile > p.S) hi = min(hi, p.S - t * kTile - kCols * g);
+    const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < kCols);
+    // Key unit: the statistics belong to the columns. In fragment form a thread has a quarter of the
     // columns (of four rows), and reads a quarter of the statistics that it would need with a whole row
-    // (B = 4, H = 32, S = 4096, causal: d = 128 1262 to 1247 us, d = 64 993 to 950 us).
-    const uint64_t* st = reinterpret_cast<const uint64_t*>(smem + C::kOffStat + (i & 1) * kStatBytes) + 32 * g +
-                         (lane & 3);
+    // (B = 4, H = 32, S = 4096, causal: d = 128 1262 to 1247 us, d = 64 993 to 950 us, with
+    // two warpgroups).
+    const uint64_t* st = reinterpret_cast<const uint64_t*>(smem + C::kOffStat + (i & 1) * kStatBytes) +
+                         kWords * g + (lane & 3);
     if (KEY) step_wait(&bars.stat_full[i & 1], (i >> 1) & 1, abort, kSiteBwdStat);
     step_wait(&bars.s[L::s_bar(i)], L::s_parity(i), abort, kSiteBwdS);
     __syncwarp();
     tc_fence_after();
-    uint64_t pr[32];  // P: 64 values in pairs
+    uint64_t pr[kCols / 2];  // P: this row's values in pairs
     const uint32_t ts = tmem + L::col_s(i) + half_off;
     // Masked tiles (few): the masked scores become -inf in TMEM, so that the path every tile takes has no
     // mask in it. P is 0 there, and so is dS (of finite dP).
     if constexpr (KEY) {
-      uint32_t sr[64];
-      tmem_ld_frag(ts, sr);
-      tmem_ld_frag(ts + (16u << 16), sr + 32);
-      uint64_t nl[8];
+      uint32_t sr[kCols];
+      tmem_ld_frag<kWords>(ts, sr);
+      tmem_ld_frag<kWords>(ts + (16u << 16), sr + kWords);
+      uint64_t nl[kCols / 8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) nl[q] = st[4 * q];
-      tmem_ld_wait(sr);
-      tmem_ld_wait(sr + 32);
+      for (int q = 0; q < kCols / 8; ++q) nl[q] = st[4 * q];
+      frag_wait<kWords>(sr);
+      frag_wait<kWords>(sr + kWords);
       if (masked) {
-        const int first_col = (lane >> 2) + (warp & 3) * 32 - 64 * g - 2 * (lane & 3);
+        const int first_col = (lane >> 2) + (warp & 3) * 32 - kCols * g - 2 * (lane & 3);
 #pragma unroll
-        for (int k = 0; k < 64; ++k)  // row 16 (k / 32) + 8 (k / 2 % 2) of this thread's four, column 8 (k / 4 % 8) + k % 2
-          if (8 * ((k >> 2) & 7) + (k & 1) < first_col + 16 * (k >> 5) + 8 * ((k >> 1) & 1)) sr[k] = 0xff800000u;
+        for (int k = 0; k < kCols; ++k)  // row 16 (k / kWords) + 8 (k / 2 % 2) of this thread's four
+          if (8 * (k % kWords >> 2) + (k & 1) < first_col + 16 * (k / kWords) + 8 * ((k >> 1) & 1)) sr[k] = 0xff800000u;
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t pk[16], rest[16];
+        uint32_t pk[kWords / 2], rest[kWords / 2];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const uint32_t* v = sr + 32 * h + 2 * k;
+        for (int k = 0; k < kWords / 2; ++k) {
+          const uint32_t* v = sr + kWords * h + 2 * k;
           float x0, x1;
           split_f32x2(fma_f32x2(f32x2(__uint_as_float(v[0]), __uint_as_float(v[1])), c2, nl[k >> 1]), x0, x1);
           x0 = ex2(x0);
           x1 = ex2(x1);
-          pr[16 * h + k] = f32x2(x0, x1);
+          pr[kWords / 2 * h + k] = f32x2(x0, x1);
           pk[k] = pack_bf16x2(x0, x1);
           if constexpr (SPLIT) rest[k] = rest_bf16x2(x0, x1, pk[k]);
         }
-        tmem_st_frag(ts + ((16u * h) << 16), pk);  // P^T is dV's A operand, written over the scores
-        if constexpr (SPLIT) tmem_st_frag(ts + ((16u * h) << 16) + 32, rest);
+        tmem_st_frag<kWords / 2>(ts + ((16u * h) << 16), pk);  // P^T is dV's A operand, written over the scores
+        if constexpr (SPLIT) tmem_st_frag<kWords / 2>(ts + ((16u * h) << 16) + kWords, rest);
       }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.p[i & 1]);
     } else {
-      uint32_t sr[64];
-      tmem_ld32(ts, sr);
-      tmem_ld32(ts + 32, sr + 32);
-      tmem_ld_wait(sr);
-      tmem_ld_wait(sr + 32);
+      uint32_t sr[kCols];
+#pragma unroll
+      for (int c = 0; c < kCols; c += 32) tmem_ld32(ts + c, sr + c);
+#pragma unroll
+      for (int c = 0; c < kCols; c += 32) tmem_ld_wait(sr + c);
       if (masked) {
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
+        for (int c = 0; c < kCols; ++c)
           if (c >= hi) sr[c] = 0xff800000u;
       }
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
+      for (int k = 0; k < kCols / 4; ++k) {
         float x0, x1, x2, x3;
         split_f32x2(fma_f32x2(f32x2(__uint_as_float(sr[4 * k]), __uint_as_float(sr[4 * k + 1])), c2, nlse2), x0, x1);
         split_f32x2(fma_f32x2(f32x2(__uint_as_float(sr[4 * k + 2]), __uint_as_float(sr[4 * k + 3])), c2, nlse2), x2, x3);
@@ -628,35 +658,35 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
     tc_fence_after();
     const uint32_t td = tmem + L::kColDp + half_off;
     if constexpr (KEY) {
-      uint32_t dr[64];
-      tmem_ld_frag(td, dr);
-      tmem_ld_frag(td + (16u << 16), dr + 32);
-      uint64_t nd[8];
+      uint32_t dr[kCols];
+      tmem_ld_frag<kWords>(td, dr);
+      tmem_ld_frag<kWords>(td + (16u << 16), dr + kWords);
+      uint64_t nd[kCols / 8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) nd[q] = st[64 + 4 * q];
-      tmem_ld_wait(dr);
-      tmem_ld_wait(dr + 32);
+      for (int q = 0; q < kCols / 8; ++q) nd[q] = st[64 + 4 * q];
+      frag_wait<kWords>(dr);
+      frag_wait<kWords>(dr + kWords);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t pk[16], rest[16];
+        uint32_t pk[kWords / 2], rest[kWords / 2];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const uint32_t* v = dr + 32 * h + 2 * k;
+        for (int k = 0; k < kWords / 2; ++k) {
+          const uint32_t* v = dr + kWords * h + 2 * k;
           float a, b;
-          split_f32x2(mul_f32x2(pr[16 * h + k], add_f32x2(f32x2(__uint_as_float(v[0]), __uint_as_float(v[1])),
+          split_f32x2(mul_f32x2(pr[kWords / 2 * h + k], add_f32x2(f32x2(__uint_as_float(v[0]), __uint_as_float(v[1])),
                                                           nd[k >> 1])), a, b);
           pk[k] = pack_bf16x2(a, b);
           if constexpr (SPLIT) rest[k] = rest_bf16x2(a, b, pk[k]);
         }
-        tmem_st_frag(td + ((16u * h) << 16), pk);  // dS^T over dP^T
-        if constexpr (SPLIT) tmem_st_frag(td + ((16u * h) << 16) + 32, rest);
+        tmem_st_frag<kWords / 2>(td + ((16u * h) << 16), pk);  // dS^T over dP^T
+        if constexpr (SPLIT) tmem_st_frag<kWords / 2>(td + ((16u * h) << 16) + kWords, rest);
       }
     } else {
-      uint32_t dr[64];
-      tmem_ld32(td, dr);
-      tmem_ld32(td + 32, dr + 32);
+      uint32_t dr[kCols];
 #pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
+      for (int c = 0; c < kCols; c += 32) tmem_ld32(td + c, dr + c);
+#pragma unroll
+      for (int cc = 0; cc < kCols / 32; ++cc) {
         uint32_t pk[16], rest[16];
         tmem_ld_wait(dr + 32 * cc);
 #pragma unroll
@@ -669,7 +699,7 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
           if constexpr (SPLIT) rest[k] = rest_bf16x2(a, b, pk[k]);
         }
         tmem_st16(ts + 16 * cc, pk);  // dS over the scores
-        if constexpr (SPLIT) tmem_st16(ts + 32 + 16 * cc, rest);
+        if constexpr (SPLIT) tmem_st16(ts + kWords + 16 * cc, rest);
       }
     }
     tmem_st_wait();
@@ -685,19 +715,27 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
   step_wait(&ctl.acc, r & 1, abort, kSiteBwdAcc);
   __syncwarp();
   tc_fence_after();
-  // Key unit: warpgroup 0 stores dV, warpgroup 1 dK; query unit: half of dQ's columns each. All of the
-  // thread's columns are read before anything is stored, so that the next unit's products may start.
-  constexpr int kCols = KEY ? D : D / 2;
-  const uint32_t tacc = tmem + lane_off + g * kCols;
+  // Key unit: the first half of the warpgroups stores dV, the other dK; query unit: dQ's columns are shared
+  // out (at d = 64 to two of the four). All of the thread's columns are read before anything is stored, so
+  // that the next unit's products may start.
+  constexpr int kOut = KEY ? 2 * D / C::kGroups : D / 2;
+  constexpr int kHalf = C::kGroups / 2;
+  if (!KEY && g >= 2) {
+    // (after the wait for the products: otherwise this warp could arrive for the next unit too before others
+    // have arrived for this one)
+    if (lane == 0) mbar_arrive(&ctl.acc_free);
+    return;
+  }
+  const uint32_t tacc = tmem + lane_off + g * kOut;
   const int heads = KEY ? p.Hkv : p.Hq;
   const int srow = u.tile * kTile + row;
-  __nv_bfloat16* base = KEY ? (g == 0 ? p.dv : p.dk) : p.dq + g * kCols;
+  __nv_bfloat16* base = KEY ? (g < kHalf ? p.dv : p.dk) + g % kHalf * kOut : p.dq + g * kOut;
   base += (((int64_t)u.b * p.S + srow) * heads + u.h) * D;
-  const float mul = (KEY && g == 0) ? 1.f : p.scale;
-  uint32_t w[kCols / 2];
-  constexpr int kLoad = kCols < 64 ? 1 : 2;  // 32-column loads in flight
+  const float mul = (KEY && g < kHalf) ? 1.f : p.scale;
+  uint32_t w[kOut / 2];
+  constexpr int kLoad = kOut < 64 ? 1 : 2;  // 32-column loads in flight
 #pragma unroll
-  for (int cc = 0; cc < kCols / 32; cc += kLoad) {
+  for (int cc = 0; cc < kOut / 32; cc += kLoad) {
     uint32_t v[32 * kLoad];
 #pragma unroll
     for (int x = 0; x < kLoad; ++x) tmem_ld32(tacc + 32 * (cc + x), v + 32 * x);
@@ -711,8 +749,8 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
   __syncwarp();
   if (lane == 0) mbar_arrive(&ctl.acc_free);
   // Rows of four lanes are exchanged so that each of the four stores 32 bytes of the same row: 128 bytes in
-  // a row per store (32 at d = 64, query unit: two lanes, 64 bytes).
-  constexpr int kUnits = kCols / 16;               // 32-byte units of this lane's row
+  // a row per store (32 columns: two lanes, 64 bytes).
+  constexpr int kUnits = kOut / 16;               // 32-byte units of this lane's row
   constexpr int kGroup = kUnits < 4 ? kUnits : 4;  // lanes that exchange
 #pragma unroll
   for (int x = 1; x < kGroup; x *= 2) {
@@ -772,7 +810,7 @@ __device__ __forceinline__ int walk_units(const BwdParams& p, Ctl<D>& ctl, F f) 
 }
 
 template <int D, bool SPLIT>
-__global__ void __launch_bounds__(kBwdThreads, 1) bwd_kernel(const __grid_constant__ BwdParams p) {
+__global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1) bwd_kernel(const __grid_constant__ BwdParams p) {
   using C = BwdCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   Ctl<D>& ctl = *reinterpret_cast<Ctl<D>*>(smem + C::kOffCtl);
@@ -793,24 +831,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1) bwd_kernel(const __grid_consta
       }
       for (int s = 0; s < 2; ++s) {
         mbar_init(&bars.s[s], 1);
-        mbar_init(&bars.p[s], 8);  // two: a warp may reach step i + 1 before another has finished step i
+        mbar_init(&bars.p[s], 4 * C::kGroups);  // two: a warp may reach step i + 1 before another has finished step i
         mbar_init(&bars.turn[s], 1);
         mbar_init(&bars.stat_full[s], 1);
-        mbar_init(&bars.stat_empty[s], 8);  // one arrival per math warp
+        mbar_init(&bars.stat_empty[s], 4 * C::kGroups);  // one arrival per math warp
       }
       mbar_init(&bars.dp, 1);
-      mbar_init(&bars.ds, 8);
+      mbar_init(&bars.ds, 4 * C::kGroups);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ctl.resp_full[s], 1);
-      mbar_init(&ctl.resp_empty[s], kBwdWalkers);
+      mbar_init(&ctl.resp_empty[s], C::kWalkers);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ctl.resident[s], 1);
       mbar_init(&ctl.res_free[s], 1);
     }
     mbar_init(&ctl.acc, 2);
-    mbar_init(&ctl.acc_free, 8);
+    mbar_init(&ctl.acc_free, 4 * C::kGroups);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -823,7 +861,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) bwd_kernel(const __grid_consta
 
   // (each register budget is set inside the branch of its role, where the compiler sees it)
   if (warp == 0) {
-    regs_dec<kRegsBwdControl>();
+    if constexpr (C::kGroups == 2) regs_dec<kRegsBwdControl>();
     Copies copies;
     walk_units<D>(p, ctl, [&](const BwdUnit& u, int r, int first, bool same) {
       if (lane != 0) return;
@@ -841,23 +879,23 @@ __global__ void __launch_bounds__(kBwdThreads, 1) bwd_kernel(const __grid_consta
     });
     if (lane == 0 && ctl.abort) drain_copies<D>(p, ctl, copies);
   } else if (warp == 1) {
-    regs_dec<kRegsBwdControl>();
+    if constexpr (C::kGroups == 2) regs_dec<kRegsBwdControl>();
     const int units = walk_units<D>(p, ctl, [&](const BwdUnit& u, int r, int first, bool same) {
       if (u.key) issue_mmas<D, SPLIT, true, 0>(p, u.steps, smem, ctl, r, first, same);
       else issue_mmas<D, SPLIT, false, 0>(p, u.steps, smem, ctl, r, first, same);
     });
     wait_products<D>(p, ctl, units);
   } else if (warp == 2) {
-    regs_dec<kRegsBwdControl>();
+    if constexpr (C::kGroups == 2) regs_dec<kRegsBwdControl>();
     const int units = walk_units<D>(p, ctl, [&](const BwdUnit& u, int r, int first, bool same) {
       if (u.key) issue_mmas<D, SPLIT, true, 1>(p, u.steps, smem, ctl, r, first, same);
       else issue_mmas<D, SPLIT, false, 1>(p, u.steps, smem, ctl, r, first, same);
     });
     wait_products<D>(p, ctl, units);
   } else if (warp == 3) {
-    regs_dec<kRegsBwdControl>();
+    if constexpr (C::kGroups == 2) regs_dec<kRegsBwdControl>();
   } else {
-    regs_inc<kRegsBwdMath>();
+    if constexpr (C::kGroups == 2) regs_inc<kRegsBwdMath>();
     walk_units<D>(p, ctl, [&](const BwdUnit& u, int r, int first, bool) {
       if (u.key) math_warps<D, SPLIT, true>(p, u, smem, ctl, r, first);
       else math_warps<D, SPLIT, false>(p, u, smem, ctl, r, first);
@@ -949,8 +987,8 @@ cudaError_t launch_bwd(const StatParams& sp, const BwdParams& p, int64_t units, 
     cudaFuncAttributes attr;
     cudaError_t e = cudaFuncGetAttributes(&attr, bwd_kernel<D, SPLIT>);
     if (e != cudaSuccess) return e;
-    pool_ok.store(attr.numRegs * kBwdThreads >= 128 * kRegsBwdControl + 256 * kRegsBwdMath ? 1 : 0,
-                  std::memory_order_relaxed);
+    const int split = BwdCfg<D>::kGroups == 2 ? 128 * kRegsBwdControl + 256 * kRegsBwdMath : 0;
+    pool_ok.store(attr.numRegs * BwdCfg<D>::kThreads >= split ? 1 : 0, std::memory_order_relaxed);
   }
   if (pool_ok.load(std::memory_order_relaxed) != 1) return cudaErrorInvalidConfiguration;
   static std::atomic<unsigned> configured_mask{0u};  // one bit per device ordinal below 32
@@ -970,7 +1008,7 @@ cudaError_t launch_bwd(const StatParams& sp, const BwdParams& p, int64_t units, 
   // a programmatic dependent of the statistics kernel: set-up and the first tile loads overlap it
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)units);
-  cfg.blockDim = dim3(kBwdThreads);
+  cfg.blockDim = dim3(BwdCfg<D>::kThreads);
   cfg.dynamicSmemBytes = BwdCfg<D>::kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr = {};
