@@ -178,11 +178,15 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
-def _one_device(index, tensors):
-    """Every tensor of a call lives on one device (None entries are absent arguments)."""
-    for name, t in tensors:
-        if t is not None and t.get_device() != index:
-            raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+def _check_tensor(name, t, shape, dtype, index):
+    """One tensor of a call: contiguous, of this shape and type, on device `index` (the shape of another
+    argument of the call, or a tuple)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda:
+        raise (TypeError if dtype is torch.bfloat16 else ValueError)(f"{name} must be a CUDA {dtype} tensor")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
 
 
 _NO_CONTEXT = contextlib.nullcontext()
@@ -195,7 +199,7 @@ def _on_device(index, stream):
         if stream.device.index != index:
             raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
         return torch.cuda.stream(stream)  # makes its device current too
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         return _NO_CONTEXT
     return torch.cuda.device(index)
 
@@ -205,23 +209,24 @@ def _handle(index, stream):
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
-def _result(name, t, shape, dtype, device):
-    """A caller-given output after its checks, or a new one."""
+def _result(name, t, shape, dtype, like):
+    """A caller-given output after its checks, or a new one (on the device of `like`)."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or t.shape != shape
-            or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != like.get_device()
+            or t.shape != shape or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {like.device}")
     return t
 
 
-def _scratch(workspace, need, device):
+def _scratch(workspace, need, like):
     """A caller-given workspace (any contiguous CUDA tensor), or a new one; with its size in bytes."""
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    elif not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return workspace, workspace.numel() * workspace.element_size()
+        return torch.empty(need, dtype=torch.uint8, device=like.device), need
+    if (not isinstance(workspace, torch.Tensor) or workspace.get_device() != like.get_device()
+            or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
+    return workspace, workspace.nbytes
 
 
 def fa_bwd_workspace_bytes(B, Hq, Hkv, S, d, causal=False):
@@ -236,31 +241,28 @@ def fa_bwd(q, k, v, out, lse, dout, causal=False, scale=None, dlse=None, dq=None
     lse are fa_fwd's results for q, k, v with the same causal and scale. dlse ([B, S, Hq] fp32) is the
     gradient with respect to lse, if a loss uses it. Returns (dq, dk, dv) in the layouts of q, k, v.
     Nothing is summed by atomics: the same inputs give the same bits."""
-    for name, t in (("q", q), ("k", k), ("v", v), ("out", out), ("dout", dout)):
-        _bf16_cuda(name, t, 4)
-    B, S, Hq, d = q.shape
-    Hkv = k.shape[2]
-    if k.shape != (B, S, Hkv, d) or v.shape != k.shape:
-        raise ValueError("k and v must be [B, S, Hkv, d] matching q")
-    if out.shape != q.shape or dout.shape != q.shape:
-        raise ValueError("out and dout must have q's shape")
-    for name, t in (("lse", lse), ("dlse", dlse)):
-        if t is None and name == "dlse":
-            continue
-        if (not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_cuda or t.shape != (B, S, Hq)
-                or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of shape {(B, S, Hq)}")
+    _bf16_cuda("q", q, 4)
+    _bf16_cuda("k", k, 4)
+    q_shape, k_shape = q.shape, k.shape
+    B, S, Hq, d = q_shape
+    Hkv = k_shape[2]
     index = q.get_device()
-    _one_device(index, (("k", k), ("v", v), ("out", out), ("lse", lse), ("dout", dout), ("dlse", dlse)))
+    _check_tensor("k", k, (B, S, Hkv, d), torch.bfloat16, index)
+    _check_tensor("v", v, k_shape, torch.bfloat16, index)
+    _check_tensor("out", out, q_shape, torch.bfloat16, index)
+    _check_tensor("dout", dout, q_shape, torch.bfloat16, index)
+    rows = (B, S, Hq)
+    _check_tensor("lse", lse, rows, torch.float32, index)
+    if dlse is not None:
+        _check_tensor("dlse", dlse, rows, torch.float32, index)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     lib = load_library()
     with _on_device(index, stream):
-        device = q.device
-        dq = _result("dq", dq, q.shape, q.dtype, device)
-        dk = _result("dk", dk, k.shape, k.dtype, device)
-        dv = _result("dv", dv, v.shape, v.dtype, device)
+        dq = _result("dq", dq, q_shape, torch.bfloat16, q)
+        dk = _result("dk", dk, k_shape, torch.bfloat16, q)
+        dv = _result("dv", dv, k_shape, torch.bfloat16, q)
         need = 0 if workspace is not None else fa_bwd_workspace_bytes(B, Hq, Hkv, S, d, causal)
-        workspace, ws_bytes = _scratch(workspace, need, device)
+        workspace, ws_bytes = _scratch(workspace, need, q)
         code = lib.fa_bwd(_address(q), _address(k), _address(v), _address(out), _address(lse), _address(dout),
                           _address(dlse), _address(dq), _address(dk), _address(dv), B, Hq, Hkv, S, d,
                           int(bool(causal)), scale, _address(workspace), ws_bytes, _handle(index, stream))
@@ -545,11 +547,10 @@ def fa_qk_norm_rope_bwd(dq_out, dk_out, q, k, positions=None, inv_freq=None, q_w
         so, sp = _token_rows("dq", dq, q_shape, wq, index), _token_rows("dk", dk, k_shape, wk, index)
         ws_bytes = 0
         if q_weight is not None:
-            device = q.device
-            dq_weight = _result("dq_weight", dq_weight, q_weight.shape, torch.float32, device)
-            dk_weight = _result("dk_weight", dk_weight, k_weight.shape, torch.float32, device)
+            dq_weight = _result("dq_weight", dq_weight, q_weight.shape, torch.float32, q)
+            dk_weight = _result("dk_weight", dk_weight, k_weight.shape, torch.float32, q)
             need = 0 if workspace is not None else fa_qk_norm_rope_bwd_workspace_bytes(T, Hq, Hkv, d)
-            workspace, ws_bytes = _scratch(workspace, need, device)
+            workspace, ws_bytes = _scratch(workspace, need, q)
         else:
             dq_weight = dk_weight = workspace = None
         code = lib.fa_qk_norm_rope_bwd(_address(dq_out), sg, _address(dk_out), sh, _address(q), sq, _address(k), sk,
