@@ -142,7 +142,7 @@ struct Ctl {
   uint4 resp[2];                           // launch cancellation responses
   uint64_t resp_full[2], resp_empty[2];
   StepBars<D> kind[2];                     // query units, key units
-  uint64_t resident[2], res_free[2], acc, acc_free;  // one phase per unit
+  uint64_t resident[2], res_free[2], acc[2], acc_free;  // one phase per unit
   uint32_t tmem;
   int abort;
 };
@@ -504,7 +504,7 @@ __device__ __forceinline__ void issue_mmas(const BwdParams& p, int n, uint8_t* s
     }
   }
   __syncwarp();
-  if (elect_one()) mma_commit(&ctl.acc);  // the barrier counts both chains
+  if (elect_one()) mma_commit(&ctl.acc[CHAIN]);
   __syncwarp();
 }
 
@@ -550,9 +550,9 @@ __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t* r) 
   }
 }
 
-// P and dS of one row's columns (this warpgroup's share) per step, then the gradients' epilogue.
+// P and dS of one row's columns (this warpgroup's share) per step.
 template <int D, bool SPLIT, bool KEY>
-__device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u, uint8_t* smem, Ctl<D>& ctl, int r,
+__device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u, uint8_t* smem, Ctl<D>& ctl,
                                            int first) {
   using C = BwdCfg<D>;
   using L = Layout<D, KEY>;
@@ -711,85 +711,105 @@ __device__ __forceinline__ void math_warps(const BwdParams& p, const BwdUnit& u,
     }
     if (++t == u.first + u.per) t = u.first;
   }
-  // ------------------------------------------------------------ epilogue
-  step_wait(&ctl.acc, r & 1, abort, kSiteBwdAcc);
-  __syncwarp();
-  tc_fence_after();
-  // Key unit: the first half of the warpgroups stores dV, the other dK; query unit: dQ's columns are shared
-  // out (at d = 64 to two of the four). All of the thread's columns are read before anything is stored, so
-  // that the next unit's products may start.
-  constexpr int kOut = KEY ? 2 * D / C::kGroups : D / 2;
-  constexpr int kHalf = C::kGroups / 2;
-  if (!KEY && g >= 2) {
-    // (after the wait for the products: otherwise this warp could arrive for the next unit too before others
-    // have arrived for this one)
-    if (lane == 0) mbar_arrive(&ctl.acc_free);
-    return;
-  }
-  const uint32_t tacc = tmem + lane_off + g * kOut;
+}
+
+// The gradients of a unit out of TMEM: accumulator 0 is dV or dQ, 1 dK. Two warpgroups share the columns of
+// an accumulator; at d = 64 the other two take dK. At d = 128 dV is stored while dK's last product runs (8 x 512
+// tokens of 16 heads, causal: 52 to 50 us).
+template <int D, bool KEY>
+__device__ __forceinline__ void store_gradients(const BwdParams& p, const BwdUnit& u, Ctl<D>& ctl, int r) {
+  using C = BwdCfg<D>;
+  volatile int* abort = &ctl.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = (warp - 4) >> 2;
+  const int row = (warp & 3) * 32 + lane;
+  constexpr int kOut = D / 2;                      // columns per thread
+  constexpr int kUnits = kOut / 16;                // 32-byte units of this lane's row
+  constexpr int kGroup = kUnits < 4 ? kUnits : 4;  // lanes that exchange
+  const uint32_t tacc = ctl.tmem + ((uint32_t)((warp & 3) * 32) << 16) + (g & 1) * kOut;
   const int heads = KEY ? p.Hkv : p.Hq;
   const int srow = u.tile * kTile + row;
-  __nv_bfloat16* base = KEY ? (g < kHalf ? p.dv : p.dk) + g % kHalf * kOut : p.dq + g * kOut;
-  base += (((int64_t)u.b * p.S + srow) * heads + u.h) * D;
-  const float mul = (KEY && g < kHalf) ? 1.f : p.scale;
-  uint32_t w[kOut / 2];
-  constexpr int kLoad = kOut < 64 ? 1 : 2;  // 32-column loads in flight
+  const int own = lane % kGroup;
+  const int64_t at = (((int64_t)u.b * p.S + srow - own) * heads + u.h) * D + (g & 1) * kOut + 16 * own;
+  auto wait_acc = [&](int x) {  // (by every warp, for each phase in turn)
+    step_wait(&ctl.acc[x], r & 1, abort, kSiteBwdAcc);
+    __syncwarp();
+    tc_fence_after();
+  };
+  auto store = [&](int x, bool last) {
+    __nv_bfloat16* base = (KEY ? (x ? p.dk : p.dv) : p.dq) + at;
+    const float mul = (KEY && !x) ? 1.f : p.scale;
+    uint32_t w[kOut / 2];
+    uint32_t v[kOut];
 #pragma unroll
-  for (int cc = 0; cc < kOut / 32; cc += kLoad) {
-    uint32_t v[32 * kLoad];
+    for (int c = 0; c < kOut; c += 32) tmem_ld32(tacc + x * D + c, v + c);
 #pragma unroll
-    for (int x = 0; x < kLoad; ++x) tmem_ld32(tacc + 32 * (cc + x), v + 32 * x);
+    for (int c = 0; c < kOut; c += 32) tmem_ld_wait(v + c);
 #pragma unroll
-    for (int x = 0; x < kLoad; ++x) tmem_ld_wait(v + 32 * x);
+    for (int k = 0; k < kOut / 2; ++k)
+      w[k] = pack_bf16x2(__uint_as_float(v[2 * k]) * mul, __uint_as_float(v[2 * k + 1]) * mul);
+    tc_fence_before();
+    __syncwarp();
+    // all of this warp's columns have been read: the next unit's products may start
+    if (lane == 0 && last) mbar_arrive(&ctl.acc_free);
+    // Rows of kGroup lanes are exchanged so that each of them stores 32 bytes of the same row: 128 bytes in a
+    // row per store (d = 64: two lanes, 64 bytes). Unit k of lane l is then unit l % kGroup of row k.
 #pragma unroll
-    for (int k = 0; k < 16 * kLoad; ++k)
-      w[16 * cc + k] = pack_bf16x2(__uint_as_float(v[2 * k]) * mul, __uint_as_float(v[2 * k + 1]) * mul);
-  }
-  tc_fence_before();
-  __syncwarp();
-  if (lane == 0) mbar_arrive(&ctl.acc_free);
-  // Rows of four lanes are exchanged so that each of the four stores 32 bytes of the same row: 128 bytes in
-  // a row per store (32 columns: two lanes, 64 bytes).
-  constexpr int kUnits = kOut / 16;               // 32-byte units of this lane's row
-  constexpr int kGroup = kUnits < 4 ? kUnits : 4;  // lanes that exchange
+    for (int y = 1; y < kGroup; y *= 2) {
+      const bool upper = lane & y;
 #pragma unroll
-  for (int x = 1; x < kGroup; x *= 2) {
-    const bool upper = lane & x;
+      for (int k = 0; k < kUnits; ++k) {
+        if (k & y) continue;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t &lo = w[8 * k + c], &hi = w[8 * (k + y) + c];
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? lo : hi, y);
+          if (upper) lo = got;
+          else hi = got;
+        }
+      }
+    }
+    const bool wide = (reinterpret_cast<uintptr_t>(base) & 31) == 0;  // (the same for every row)
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
-      if (k & x) continue;
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        uint32_t &lo = w[8 * k + c], &hi = w[8 * (k + x) + c];
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? lo : hi, x);
-        if (upper) lo = got;
-        else hi = got;
+      __nv_bfloat16* dst = base + (int64_t)k * heads * D;
+      if (srow - own + k < p.S) {
+        if (wide) {
+          st_global_32(dst, w + 8 * k);
+        } else {
+          *reinterpret_cast<uint4*>(dst) = make_uint4(w[8 * k], w[8 * k + 1], w[8 * k + 2], w[8 * k + 3]);
+          *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[8 * k + 4], w[8 * k + 5], w[8 * k + 6], w[8 * k + 7]);
+        }
       }
     }
-  }
-  // unit k of lane l is now unit (k / kGroup) kGroup + l % kGroup of row k % kGroup of its group
-  const int own = lane % kGroup;
-  __nv_bfloat16* rows = base - (int64_t)own * heads * D + 16 * own;
-  const bool wide = (reinterpret_cast<uintptr_t>(base) & 31) == 0;  // (the same for every row)
-#pragma unroll
-  for (int k = 0; k < kUnits; ++k) {
-    __nv_bfloat16* dst = rows + (int64_t)(k % kGroup) * heads * D + 16 * (k / kGroup) * kGroup;
-    if (srow - own + k % kGroup < p.S) {
-      if (wide) {
-        st_global_32(dst, w + 8 * k);
-      } else {
-        *reinterpret_cast<uint4*>(dst) = make_uint4(w[8 * k], w[8 * k + 1], w[8 * k + 2], w[8 * k + 3]);
-        *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[8 * k + 4], w[8 * k + 5], w[8 * k + 6], w[8 * k + 7]);
+  };
+  if constexpr (C::kGroups == 2) {
+    if constexpr (KEY) {
+#pragma unroll 1
+      for (int x = 0; x < 2; ++x) {
+        wait_acc(x);
+        store(x, x == 1);
       }
+    } else {
+      wait_acc(0);
+      store(0, true);
+      wait_acc(1);
     }
+  } else {
+    wait_acc(0);
+    wait_acc(1);
+    // (A warp without columns too arrives after the products: earlier, it could arrive for the next unit before
+    // others have arrived for this one.)
+    if (KEY || g < 2) store(g >> 1, true);
+    else if (lane == 0) mbar_arrive(&ctl.acc_free);
   }
 }
 
-// Every product has completed (before TMEM is released; after an abort nobody else waits for them).
+// The chain's products have completed (before TMEM is released; after an abort nobody else waits for them).
 template <int D>
-__device__ __forceinline__ void wait_products(const BwdParams& p, Ctl<D>& ctl, int units) {
+__device__ __forceinline__ void wait_products(Ctl<D>& ctl, int chain, int units) {
   int no_abort = 0;
-  step_wait(&ctl.acc, (units - 1) & 1, &no_abort, kSiteBwdDrain);
+  step_wait(&ctl.acc[chain], (units - 1) & 1, &no_abort, kSiteBwdDrain);
 }
 
 // A warp's walk over the CTA's units: f(unit, units before it, steps before it in units of its kind,
@@ -846,8 +866,8 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1) bwd_kernel(const __gri
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ctl.resident[s], 1);
       mbar_init(&ctl.res_free[s], 1);
+      mbar_init(&ctl.acc[s], 1);
     }
-    mbar_init(&ctl.acc, 2);
     mbar_init(&ctl.acc_free, 4 * C::kGroups);
     fence_mbar_init();
   }
@@ -884,21 +904,26 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1) bwd_kernel(const __gri
       if (u.key) issue_mmas<D, SPLIT, true, 0>(p, u.steps, smem, ctl, r, first, same);
       else issue_mmas<D, SPLIT, false, 0>(p, u.steps, smem, ctl, r, first, same);
     });
-    wait_products<D>(p, ctl, units);
+    wait_products<D>(ctl, 0, units);
   } else if (warp == 2) {
     if constexpr (C::kGroups == 2) regs_dec<kRegsBwdControl>();
     const int units = walk_units<D>(p, ctl, [&](const BwdUnit& u, int r, int first, bool same) {
       if (u.key) issue_mmas<D, SPLIT, true, 1>(p, u.steps, smem, ctl, r, first, same);
       else issue_mmas<D, SPLIT, false, 1>(p, u.steps, smem, ctl, r, first, same);
     });
-    wait_products<D>(p, ctl, units);
+    wait_products<D>(ctl, 1, units);
   } else if (warp == 3) {
     if constexpr (C::kGroups == 2) regs_dec<kRegsBwdControl>();
   } else {
     if constexpr (C::kGroups == 2) regs_inc<kRegsBwdMath>();
     walk_units<D>(p, ctl, [&](const BwdUnit& u, int r, int first, bool) {
-      if (u.key) math_warps<D, SPLIT, true>(p, u, smem, ctl, r, first);
-      else math_warps<D, SPLIT, false>(p, u, smem, ctl, r, first);
+      if (u.key) {
+        math_warps<D, SPLIT, true>(p, u, smem, ctl, first);
+        store_gradients<D, true>(p, u, ctl, r);
+      } else {
+        math_warps<D, SPLIT, false>(p, u, smem, ctl, first);
+        store_gradients<D, false>(p, u, ctl, r);
+      }
     });
   }
   tc_fence_before();
